@@ -39,6 +39,24 @@ class NsaConfig(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class NsaWindowConfig(ctypes.Structure):
+    """Mirror of ``nsa_window_config`` in include/nsa.h."""
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen_q", ctypes.c_int32),
+                ("seqlen_kv", ctypes.c_int32), ("q_pos0", ctypes.c_int32),
+                ("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d_qk", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("window", ctypes.c_int32), ("sink", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class NsaPagedConfig(ctypes.Structure):
+    """Mirror of ``nsa_paged_config`` in include/nsa.h."""
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen_q", ctypes.c_int32), ("h_q", ctypes.c_int32),
+                ("h_kv", ctypes.c_int32), ("d_qk", ctypes.c_int32), ("d_v", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32), ("sink", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
 class NsaError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -50,6 +68,8 @@ class NsaError(RuntimeError):
 
 _vp, _sz = ctypes.c_void_p, ctypes.c_size_t
 _cfgp = ctypes.POINTER(NsaConfig)
+_wcfgp = ctypes.POINTER(NsaWindowConfig)
+_pcfgp = ctypes.POINTER(NsaPagedConfig)
 _SIGS = {
     "nsa_workspace_size": [_cfgp, ctypes.POINTER(_sz)],
     "nsa_workspace_size_min": [_cfgp, ctypes.POINTER(_sz)],
@@ -72,6 +92,17 @@ _SIGS = {
                             _sz, _vp],
     "nsa_timing_read": [ctypes.c_int32, ctypes.POINTER(ctypes.c_float),
                         ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_int32)],
+    "nsa_window_attn_fwd": [_wcfgp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "nsa_window_bwd_workspace_size": [_wcfgp, ctypes.POINTER(_sz)],
+    "nsa_window_attn_bwd": [_wcfgp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "nsa_paged_workspace_size": [_pcfgp, ctypes.POINTER(_sz)],
+    "nsa_paged_attn_fwd": [_pcfgp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "nsa_paged_append_workspace_size": [_pcfgp, ctypes.POINTER(_sz)],
+    "nsa_paged_append": [_pcfgp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+    "nsa_pages_fork": [_pcfgp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "nsa_pages_free": [_pcfgp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "nsa_pages_compact_workspace_size": [_pcfgp, ctypes.POINTER(_sz)],
+    "nsa_pages_compact": [_pcfgp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
 }
 for _name, _args in _SIGS.items():
     _f = getattr(lib, _name)
@@ -286,3 +317,209 @@ def forward(cfg: NsaConfig, q, k, v, gates=None, idx=None, stream=None, pooled=N
     nsa_sparse_attn_fwd(cfg, q, k, v, pooled["kbar"], pooled["kcmp"], pooled["vcmp"], gates, idx,
                         out, workspace, ws, stream)
     return out, pooled
+
+
+# ---------------------------------------------------------------------------
+# Window attention with sink tokens, and the paged cache
+# ---------------------------------------------------------------------------
+
+def window_config(batch, seqlen_q, seqlen_kv, h_q, h_kv, d_qk, d_v, window, sink=0, q_pos0=0,
+                  scale=None) -> NsaWindowConfig:
+    """nsa_window_config (scale: 1/sqrt(d_qk) unless given)."""
+    return NsaWindowConfig(batch, seqlen_q, seqlen_kv, q_pos0, h_q, h_kv, d_qk, d_v, window, sink,
+                           max(d_qk, 1) ** -0.5 if scale is None else scale, 0)
+
+
+def paged_config(batch, seqlen_q, h_q, h_kv, d_qk, d_v, page_size, n_pages, max_pages, window=0,
+                 sink=0, scale=None) -> NsaPagedConfig:
+    """nsa_paged_config (scale: 1/sqrt(d_qk) unless given)."""
+    return NsaPagedConfig(batch, seqlen_q, h_q, h_kv, d_qk, d_v, page_size, n_pages, max_pages,
+                          window, sink, max(d_qk, 1) ** -0.5 if scale is None else scale, 0)
+
+
+def nsa_window_attn_fwd(cfg, q, k, v, out, lse=None, stream=None):
+    _check("nsa_window_attn_fwd",
+           lib.nsa_window_attn_fwd(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                   _ptr(lse), _stream(stream)))
+
+
+def nsa_window_bwd_workspace_size(cfg) -> int:
+    n = _sz(0)
+    _check("nsa_window_bwd_workspace_size",
+           lib.nsa_window_bwd_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def nsa_window_attn_bwd(cfg, q, k, v, out, lse, d_out, dq, dk, dv, workspace=None, ws_bytes=0,
+                        stream=None):
+    _check("nsa_window_attn_bwd",
+           lib.nsa_window_attn_bwd(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                   _ptr(lse), _ptr(d_out), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def nsa_paged_workspace_size(cfg) -> int:
+    n = _sz(0)
+    _check("nsa_paged_workspace_size",
+           lib.nsa_paged_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def nsa_paged_attn_fwd(cfg, q, k_pages, v_pages, table, lens, out, lse=None, workspace=None,
+                       ws_bytes=0, stream=None):
+    _check("nsa_paged_attn_fwd",
+           lib.nsa_paged_attn_fwd(ctypes.byref(cfg), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+                                  _ptr(table), _ptr(lens), _ptr(out), _ptr(lse), _ptr(workspace),
+                                  ws_bytes, _stream(stream)))
+
+
+def nsa_paged_append_workspace_size(cfg) -> int:
+    n = _sz(0)
+    _check("nsa_paged_append_workspace_size",
+           lib.nsa_paged_append_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def nsa_paged_append(cfg, k_new, v_new, n_new, k_pages, v_pages, table, lens, ref, short_pages,
+                     workspace=None, ws_bytes=0, stream=None):
+    _check("nsa_paged_append",
+           lib.nsa_paged_append(ctypes.byref(cfg), _ptr(k_new), _ptr(v_new), _ptr(n_new),
+                                _ptr(k_pages), _ptr(v_pages), _ptr(table), _ptr(lens), _ptr(ref),
+                                _ptr(short_pages), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def nsa_pages_fork(cfg, n, src, dst, table, lens, ref, done, stream=None):
+    _check("nsa_pages_fork",
+           lib.nsa_pages_fork(ctypes.byref(cfg), n, _ptr(src), _ptr(dst), _ptr(table), _ptr(lens),
+                              _ptr(ref), _ptr(done), _stream(stream)))
+
+
+def nsa_pages_free(cfg, n, rows, keep, table, lens, ref, done, stream=None):
+    _check("nsa_pages_free",
+           lib.nsa_pages_free(ctypes.byref(cfg), n, _ptr(rows), _ptr(keep), _ptr(table), _ptr(lens),
+                              _ptr(ref), _ptr(done), _stream(stream)))
+
+
+def nsa_pages_compact_workspace_size(cfg) -> int:
+    n = _sz(0)
+    _check("nsa_pages_compact_workspace_size",
+           lib.nsa_pages_compact_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def nsa_pages_compact(cfg, k_pages, v_pages, table, lens, ref, remap, n_live, workspace=None,
+                      ws_bytes=0, stream=None):
+    _check("nsa_pages_compact",
+           lib.nsa_pages_compact(ctypes.byref(cfg), _ptr(k_pages), _ptr(v_pages), _ptr(table),
+                                 _ptr(lens), _ptr(ref), _ptr(remap), _ptr(n_live),
+                                 _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def _on(*named):
+    """Checks (name, tensor, shape, dtype) tuples: dense tensors of one CUDA device, which becomes
+    the current one inside the returned context."""
+    dev = named[0][1].device
+    for name, t, shape, dtype in named:
+        if t.device != dev or dev.type != "cuda":
+            raise ValueError(f"{name} is on {t.device}: all tensors belong on one CUDA device")
+        if t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}: expected {dtype} {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+    return torch.cuda.device(dev)
+
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def window_forward(cfg: NsaWindowConfig, q, k, v):
+    """Window attention with sink tokens on the current stream: (out bf16, lse fp32)."""
+    B, Tq, Hq, Tk = cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.seqlen_kv
+    with _on(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), ("k", k, (B, cfg.h_kv, Tk, cfg.d_qk), _BF16),
+             ("v", v, (B, cfg.h_kv, Tk, cfg.d_v), _BF16)):
+        out = torch.empty(B, Tq, Hq, cfg.d_v, dtype=_BF16, device=q.device)
+        lse = torch.empty(B, Tq, Hq, dtype=_F32, device=q.device)
+        nsa_window_attn_fwd(cfg, q, k, v, out, lse)
+    return out, lse
+
+
+def window_backward(cfg: NsaWindowConfig, q, k, v, out, lse, d_out):
+    """Gradients (dq, dk, dv), bf16, of window_forward on the current stream."""
+    B, Tq, Hq, Tk = cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.seqlen_kv
+    o_shape = (B, Tq, Hq, cfg.d_v)
+    with _on(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), ("k", k, (B, cfg.h_kv, Tk, cfg.d_qk), _BF16),
+             ("v", v, (B, cfg.h_kv, Tk, cfg.d_v), _BF16), ("out", out, o_shape, _BF16),
+             ("lse", lse, (B, Tq, Hq), _F32), ("d_out", d_out, o_shape, _BF16)):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = torch.empty(nsa_window_bwd_workspace_size(cfg), dtype=torch.uint8, device=q.device)
+        nsa_window_attn_bwd(cfg, q, k, v, out, lse, d_out, dq, dk, dv, ws, ws.numel())
+    return dq, dk, dv
+
+
+def _cache(cfg, k_pages, v_pages):
+    plane = (cfg.n_pages, cfg.h_kv, cfg.page_size)
+    return (("k_pages", k_pages, plane + (cfg.d_qk,), _BF16),
+            ("v_pages", v_pages, plane + (cfg.d_v,), _BF16))
+
+
+def _books(cfg, table, lens, ref=None):
+    t = (("table", table, (cfg.batch, cfg.max_pages), _I32), ("lens", lens, (cfg.batch,), _I32))
+    return t if ref is None else t + (("ref", ref, (cfg.n_pages,), _I32),)
+
+
+def paged_attention(cfg: NsaPagedConfig, q, k_pages, v_pages, table, lens):
+    """Attention of the newest cfg.seqlen_q tokens over the paged cache on the current stream:
+    (out bf16, lse fp32)."""
+    B, Tq, Hq = cfg.batch, cfg.seqlen_q, cfg.h_q
+    with _on(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), *_cache(cfg, k_pages, v_pages),
+             *_books(cfg, table, lens)):
+        out = torch.empty(B, Tq, Hq, cfg.d_v, dtype=_BF16, device=q.device)
+        lse = torch.empty(B, Tq, Hq, dtype=_F32, device=q.device)
+        ws = torch.empty(nsa_paged_workspace_size(cfg), dtype=torch.uint8, device=q.device)
+        nsa_paged_attn_fwd(cfg, q, k_pages, v_pages, table, lens, out, lse, ws, ws.numel())
+    return out, lse
+
+
+def paged_append(cfg: NsaPagedConfig, k_new, v_new, k_pages, v_pages, table, lens, ref, n_new=None):
+    """Appends up to cfg.seqlen_q tokens per sequence, in place, on the current stream.  Returns
+    short_pages [1] int32 on the device: 0, or what was missing (then nothing has changed)."""
+    new = (cfg.batch, cfg.h_kv, cfg.seqlen_q)
+    extra = () if n_new is None else (("n_new", n_new, (cfg.batch,), _I32),)
+    with _on(("k_new", k_new, new + (cfg.d_qk,), _BF16), ("v_new", v_new, new + (cfg.d_v,), _BF16),
+             *_cache(cfg, k_pages, v_pages), *_books(cfg, table, lens, ref), *extra):
+        short = torch.empty(1, dtype=_I32, device=k_new.device)
+        ws = torch.empty(nsa_paged_append_workspace_size(cfg), dtype=torch.uint8,
+                         device=k_new.device)
+        nsa_paged_append(cfg, k_new, v_new, n_new, k_pages, v_pages, table, lens, ref, short, ws,
+                         ws.numel())
+    return short
+
+
+def pages_fork(cfg: NsaPagedConfig, src, dst, table, lens, ref):
+    """Rows dst share the pages of rows src; returns done [n] int32 (1: carried out)."""
+    n = src.numel()
+    with _on(("src", src, (n,), _I32), ("dst", dst, (n,), _I32), *_books(cfg, table, lens, ref)):
+        done = torch.empty(n, dtype=_I32, device=src.device)
+        nsa_pages_fork(cfg, n, src, dst, table, lens, ref, done)
+    return done
+
+
+def pages_free(cfg: NsaPagedConfig, rows, table, lens, ref, keep=None):
+    """Rows keep their first keep tokens (None: none); returns done [n] int32."""
+    n = rows.numel()
+    extra = () if keep is None else (("keep", keep, (n,), _I32),)
+    with _on(("rows", rows, (n,), _I32), *_books(cfg, table, lens, ref), *extra):
+        done = torch.empty(n, dtype=_I32, device=rows.device)
+        nsa_pages_free(cfg, n, rows, keep, table, lens, ref, done)
+    return done
+
+
+def pages_compact(cfg: NsaPagedConfig, k_pages, v_pages, table, lens, ref):
+    """Moves the pages in use to the lowest ids, in place; returns (remap [n_pages], n_live [1])."""
+    with _on(*_cache(cfg, k_pages, v_pages), *_books(cfg, table, lens, ref)):
+        dev = table.device
+        remap = torch.empty(cfg.n_pages, dtype=_I32, device=dev)
+        n_live = torch.empty(1, dtype=_I32, device=dev)
+        ws = torch.empty(nsa_pages_compact_workspace_size(cfg), dtype=torch.uint8, device=dev)
+        nsa_pages_compact(cfg, k_pages, v_pages, table, lens, ref, remap, n_live, ws, ws.numel())
+    return remap, n_live

@@ -1,0 +1,15 @@
+// What the entry points' host-side checks share.
+#pragma once
+
+#include "common.cuh"
+
+namespace nsa {
+
+inline bool aligned16(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool supported_dqk(int d) { return d == 64 || d == 128 || d == 192 || d == 256; }
+inline bool supported_dv(int d) { return d == 64 || d == 128 || d == 256; }
+
+// NSA_OK or NSA_ERR_CUDA, remembering the error for nsa_last_cuda_error (nsa_abi.cu).
+nsa_status cuda_status(cudaError_t e);
+
+}  // namespace nsa

@@ -10,17 +10,16 @@
 #include <algorithm>
 
 #include <nvtx3/nvToolsExt.h>
-#include "common.cuh"
+#include "abi_checks.cuh"
 #include "sel_index.cuh"
 
 namespace {
 
 using nsa::Shape;
-
-bool aligned16(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool supported_dqk(int d) { return d == 64 || d == 128 || d == 192 || d == 256; }
-bool supported_dv(int d) { return d == 64 || d == 128 || d == 256; }
+using nsa::aligned16;
+using nsa::cuda_status;
+using nsa::supported_dqk;
+using nsa::supported_dv;
 
 // Validates `cfg` and fills the derived sizes.
 nsa_status make_shape(const nsa_config* cfg, Shape* s) {
@@ -202,12 +201,6 @@ WsLayout ws_layout(const Shape& s) {
 
 thread_local const char* g_last_cuda_error = "no error";
 
-nsa_status cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return NSA_OK;
-    g_last_cuda_error = cudaGetErrorString(e);
-    return NSA_ERR_CUDA;
-}
-
 // Per-host-thread stage events for nsa_timing_enable / nsa_timing_read.  The
 // same stage boundaries open and close NVTX ranges (one per stage inside one
 // per call), which a profiler attached to the process shows on its timeline;
@@ -268,6 +261,12 @@ struct TimingScope {
 };
 
 }  // namespace
+
+nsa_status nsa::cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return NSA_OK;
+    g_last_cuda_error = cudaGetErrorString(e);
+    return NSA_ERR_CUDA;
+}
 
 extern "C" {
 

@@ -1,0 +1,28 @@
+// Sliding-window attention with sink tokens: derived sizes and launchers.
+#pragma once
+
+#include "common.cuh"
+
+namespace nsa {
+
+// Sizes of one problem, window and sink clamped to the cache.
+struct WinShape {
+    int B, Tq, Tk, q0, Hq, Hkv, G, dqk, dv;
+    int win;      // 1 .. Tk
+    int ns;       // 0 .. Tk
+    float scale;
+};
+
+// Key u is visible to the query at position t.
+__host__ __device__ __forceinline__ bool win_visible(const WinShape& s, int t, int u) {
+    return u <= t && (u > t - s.win || u < s.ns);
+}
+
+// Any shape: FFMA, one warp per row (window_rowwise.cu).  delta [B, Tq, Hq].
+cudaError_t launch_window_rowwise_fwd(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                      const __nv_bfloat16* v, __nv_bfloat16* out, float* lse, cudaStream_t st);
+cudaError_t launch_window_rowwise_bwd(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                      const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
+                                      const __nv_bfloat16* d_out, __nv_bfloat16* dq, __nv_bfloat16* dk,
+                                      __nv_bfloat16* dv, float* delta, cudaStream_t st);
+}  // namespace nsa

@@ -313,6 +313,174 @@ nsa_status nsa_sparse_attn_bwd(const nsa_config* cfg, const void* q, const void*
                                void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Sliding-window attention with sink tokens
+ * -----------------------------------------
+ * Transcript #94 §4 (the sliding window and the attention sink at the start of
+ * the sequence) as one softmax of its own, for layers that are not block
+ * sparse: a query at KV position t sees the keys
+ *   vis(t) = { u <= t : u > t - window  or  u < sink },
+ * itself included, so no row is empty.  window >= seqlen_kv is full causal
+ * attention (the full-attention layers of §7's hybrid).  Layouts, positions
+ * and group sharing are those of the other entry points: q [B, Tq, Hq, d_qk],
+ * k / v [B, Hkv, Tkv, d], query i at position q_pos0 + i, head h reading KV
+ * head h / (Hq/Hkv); any number of heads per group.
+ */
+typedef struct {
+    int32_t batch;       /* B: independent sequences */
+    int32_t seqlen_q;    /* Tq: queries per sequence */
+    int32_t seqlen_kv;   /* Tkv: keys/values per sequence */
+    int32_t q_pos0;      /* KV position of query 0; q_pos0 + Tq <= Tkv */
+    int32_t h_q;         /* Hq: query heads */
+    int32_t h_kv;        /* Hkv: key/value heads */
+    int32_t d_qk;        /* query/key head dimension: 64, 128, 192 or 256 */
+    int32_t d_v;         /* value head dimension: 64, 128 or 256 */
+    int32_t window;      /* keys [t - window + 1, t]; >= 1 */
+    int32_t sink;        /* leading tokens that stay visible; >= 0 */
+    float scale;         /* logit scale, > 0, normally 1/sqrt(d_qk) */
+    uint32_t flags;      /* 0 */
+} nsa_window_config;
+
+/*
+ * Forward.  With s_u = scale * q . k_u over vis(t):
+ *   lse [B, Tq, Hq]      fp32  ln sum_u exp(s_u)      (may be NULL)
+ *   out [B, Tq, Hq, d_v] bf16  sum_u exp(s_u - lse) v_u
+ * bf16 inputs; scores, softmax statistics and sums in fp32.  On the tensor
+ * cores (d_qk <= 192, d_v <= 128, at most 64 heads per group) the weights
+ * enter the value product rounded to bf16 (relative 2^-8 at most, half a step)
+ * while their sum is taken unrounded; other shapes run on FFMA without that
+ * rounding.  k and v must be finite at every row of the cache, masked rows
+ * included: a masked key enters the value product with weight 0.
+ * Needs no workspace.
+ */
+nsa_status nsa_window_attn_fwd(const nsa_window_config* cfg, const void* q, const void* k, const void* v,
+                               void* out, float* lse, void* stream);
+
+/*
+ * Backward of the loss sum(d_out * out), from the forward's inputs and its
+ * out and lse.  With p_u = exp(s_u - lse), delta = d_out . out:
+ *   ds_u = p_u (d_out . v_u - delta)
+ *   dq [B, Tq, Hq, d_qk] = scale sum_u ds_u k_u
+ *   dk [B, Hkv, Tkv, d_qk] = scale sum_{t, h} ds_u q      dv_u = sum_{t, h} p_u d_out
+ * all bf16 and overwritten (rows of dk / dv that no query sees get 0), summed
+ * in fp32 over the group's heads and every query and rounded once at the end.
+ * No atomics: the same inputs give the same bits.  Needs
+ * nsa_window_bwd_workspace_size() bytes of workspace (delta, and the partial
+ * sums of keys that many queries see); nothing in it needs to start at zero.
+ * Every row of q, k, v, out and d_out must be finite, padded ones included
+ * (a padded query's d_out is 0).
+ */
+nsa_status nsa_window_bwd_workspace_size(const nsa_window_config* cfg, size_t* bytes);
+nsa_status nsa_window_attn_bwd(const nsa_window_config* cfg, const void* q, const void* k, const void* v,
+                               const void* out, const float* lse, const void* d_out, void* dq, void* dk,
+                               void* dv, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * A paged key/value cache
+ * -----------------------
+ * The cache is a pool of pages of page_size tokens, and a table that lists
+ * every sequence's pages in order.  All of it is caller-owned device memory:
+ *   k_pages [n_pages, Hkv, page_size, d_qk] bf16
+ *   v_pages [n_pages, Hkv, page_size, d_v]  bf16
+ *   table   [batch, max_pages]  int32  page ids; the first ceil(len/page_size)
+ *                                      entries of a row are in use
+ *   lens    [batch]             int32  tokens of each sequence (0: an empty row)
+ *   ref     [n_pages]           int32  table entries in use that name the page;
+ *                                      0: the page is free
+ * Several rows may share a page (a fork).  Values in rows of a page behind a
+ * sequence's end are never used, whatever they hold.  Ids outside
+ * [0, n_pages) in a used entry and lengths outside [0, max_pages * page_size]
+ * break the rules above; the kernels do not follow them out of bounds (such an
+ * id reads as rows of zeros and is not written, lengths are clamped), but what
+ * they compute is then unspecified.
+ * Calls on one cache are ordered by the caller (one stream).
+ */
+typedef struct {
+    int32_t batch;       /* rows of the table */
+    int32_t seqlen_q;    /* new tokens / queries per sequence (at most) */
+    int32_t h_q;         /* query heads */
+    int32_t h_kv;        /* key/value heads */
+    int32_t d_qk;        /* 64, 128, 192 or 256 */
+    int32_t d_v;         /* 64, 128 or 256 */
+    int32_t page_size;   /* tokens per page: 16, 32, 64, 128 or 256 */
+    int32_t n_pages;     /* pages of the pool */
+    int32_t max_pages;   /* columns of the table */
+    int32_t window;      /* attention: keys [t - window + 1, t]; 0: every key up to t */
+    int32_t sink;        /* attention: leading tokens that stay visible; >= 0 */
+    float scale;         /* logit scale, > 0 */
+    uint32_t flags;      /* 0 */
+} nsa_paged_config;
+
+/*
+ * Attention of the newest tokens over the paged cache (transcript #94 §6:
+ * decoding costs the KV bytes it reads).  The seqlen_q queries of sequence b
+ * sit at positions lens[b] - seqlen_q .. lens[b] - 1 (their keys are in the
+ * cache already), each seeing vis(t) as above (window 0: every key up to t):
+ *   q   [batch, seqlen_q, Hq, d_qk] bf16
+ *   out [batch, seqlen_q, Hq, d_v]  bf16     lse [batch, seqlen_q, Hq] fp32 (may be NULL)
+ * A query without keys (an empty sequence, a position below 0) gets out = 0
+ * and lse = -inf.  The work is cut over the keys of all sequences by the
+ * lengths found on the device, so one captured graph serves a growing cache;
+ * the shares of one query are joined by their log-sum-exps in fp32, in a fixed
+ * order.  Weights enter the value product rounded to bf16.  Needs
+ * nsa_paged_workspace_size() bytes of workspace, which need not start at zero.
+ */
+nsa_status nsa_paged_workspace_size(const nsa_paged_config* cfg, size_t* bytes);
+nsa_status nsa_paged_attn_fwd(const nsa_paged_config* cfg, const void* q, const void* k_pages,
+                              const void* v_pages, const int32_t* table, const int32_t* lens, void* out,
+                              float* lse, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Appends n_new[b] tokens (clamped to [0, seqlen_q]; n_new NULL: seqlen_q) to every sequence b:
+ *   k_new [batch, Hkv, seqlen_q, d_qk] bf16, v_new [batch, Hkv, seqlen_q, d_v] bf16.
+ * Rows take the pages they need, row by row and in the order of their
+ * columns, always the lowest free id; a last page that is not full and that
+ * other rows share is copied first (its filled rows), so the others never see
+ * the new tokens: of the rows that append to the same shared page in one call,
+ * each but the last takes a copy, and the last as well if a row that appends
+ * nothing still holds the page.  lens grows by n_new; table and ref follow.
+ * All or nothing: *short_pages receives 0, or the number of pages the call was
+ * short of (or -1 if a row would outgrow max_pages), and then nothing has
+ * changed.  Limits: batch <= 8192.
+ */
+nsa_status nsa_paged_append_workspace_size(const nsa_paged_config* cfg, size_t* bytes);
+nsa_status nsa_paged_append(const nsa_paged_config* cfg, const void* k_new, const void* v_new,
+                            const int32_t* n_new, void* k_pages, void* v_pages, int32_t* table, int32_t* lens,
+                            int32_t* ref, int32_t* short_pages, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Forks sequences: row dst[i] of the table becomes a second holder of row
+ * src[i]'s pages (ref grows by one each), with its length; nothing is copied
+ * until one of them appends.  src, dst [n] int32 on the device.  Entry i is
+ * carried out, and done[i] = 1, if src[i] and dst[i] are rows of the table,
+ * row dst[i] is empty, and neither an earlier entry has the same dst nor any
+ * entry has src[i] as its dst; otherwise it changes nothing and done[i] = 0.
+ */
+nsa_status nsa_pages_fork(const nsa_paged_config* cfg, int32_t n, const int32_t* src, const int32_t* dst,
+                          int32_t* table, int32_t* lens, int32_t* ref, int32_t* done, void* stream);
+
+/*
+ * Shortens sequences: row rows[i] keeps its first keep[i] tokens (keep NULL:
+ * none; a keep outside [0, length) keeps all), the pages behind them lose one
+ * holder and their entries become -1.  A page whose last holder goes is free.
+ * Entries that are no row of the table, and repeated ones, are skipped
+ * (done[i] = 0, otherwise 1).
+ */
+nsa_status nsa_pages_free(const nsa_paged_config* cfg, int32_t n, const int32_t* rows, const int32_t* keep,
+                          int32_t* table, int32_t* lens, int32_t* ref, int32_t* done, void* stream);
+
+/*
+ * Compacts the pool: afterwards the pages in use are 0 .. n_live - 1.  The
+ * i-th used page with an id >= n_live (ascending) moves into the i-th free
+ * page below n_live; the others stay.  Moved pages are copied whole, table and
+ * ref follow, and remap [n_pages] holds every page's new id (-1: it was free).
+ * n_live [1] receives the number of pages in use.
+ */
+nsa_status nsa_pages_compact_workspace_size(const nsa_paged_config* cfg, size_t* bytes);
+nsa_status nsa_pages_compact(const nsa_paged_config* cfg, void* k_pages, void* v_pages, int32_t* table,
+                             const int32_t* lens, int32_t* ref, int32_t* remap, int32_t* n_live,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Reads and clears the device-side status word of the tensor-core kernels:
  * NSA_OK, or NSA_ERR_TIMEOUT when a bounded wait inside a kernel gave up (the
  * kernel then unwound without finishing its output).  Synchronous: waits for

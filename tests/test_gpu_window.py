@@ -1,0 +1,144 @@
+"""Window attention with sink tokens (nsa_window_attn_fwd / _bwd) against the 64-bit definition."""
+import pytest
+import torch
+
+from dynamic_block_sparse_scoring_b200 import abi
+from tests.window_ref import check, visible, window_ref
+
+pytestmark = pytest.mark.gpu
+
+# batch, Tq, Tk - Tq - pos0 rows behind, q_pos0, h_q, h_kv, d_qk, d_v, window, sink
+CASES = {
+    "one_token": (1, 1, 0, 0, 4, 1, 64, 64, 1, 0),
+    "one_token_late": (2, 1, 0, 300, 16, 2, 128, 128, 100, 3),
+    "two_tokens_window_1": (1, 2, 0, 0, 2, 2, 64, 128, 1, 0),
+    "window_1_sinks": (1, 70, 0, 0, 4, 2, 128, 64, 1, 5),
+    "tiny": (1, 333, 0, 0, 4, 1, 64, 64, 128, 4),
+    "gqa16_192": (1, 200, 0, 0, 32, 2, 192, 128, 50, 7),
+    "mha": (2, 300, 0, 0, 3, 3, 128, 128, 130, 16),
+    "group_3": (1, 190, 0, 0, 6, 2, 128, 128, 64, 1),
+    "group_6": (1, 150, 0, 0, 12, 2, 192, 128, 64, 70),
+    "group_12_192_64": (1, 129, 0, 0, 12, 1, 192, 64, 40, 2),
+    "group_64": (1, 67, 0, 0, 64, 1, 128, 128, 20, 3),
+    "group_72": (1, 40, 0, 0, 72, 1, 64, 64, 20, 3),
+    "full_causal": (1, 400, 0, 0, 4, 2, 128, 128, 400, 0),
+    "window_over_cache": (1, 257, 0, 0, 4, 4, 64, 64, 100000, 9),
+    "all_sinks": (1, 260, 0, 0, 4, 2, 128, 128, 3, 1000),
+    "sinks_meet_window": (1, 300, 0, 0, 4, 2, 128, 128, 64, 65),
+    "long_window_edges": (1, 513, 0, 0, 2, 1, 128, 128, 128, 128),
+    "chunk": (2, 100, 0, 411, 8, 2, 192, 128, 150, 20),
+    "chunk_rows_behind": (2, 90, 77, 300, 8, 2, 128, 128, 128, 10),
+    "d256": (1, 90, 0, 0, 4, 2, 256, 256, 33, 4),
+    "d256_v64": (2, 61, 5, 40, 2, 1, 256, 64, 30, 4),
+    "many_key_tiles": (1, 1500, 0, 0, 8, 1, 64, 64, 700, 40),
+}
+
+
+def make(name, seed=0, spread=1.0):
+    B, Tq, behind, q0, Hq, Hkv, dqk, dv, W, ns = CASES[name]
+    Tk = q0 + Tq + behind
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    r = lambda *s: (torch.randn(*s, generator=g, device="cuda") * spread).to(torch.bfloat16)  # noqa: E731
+    cfg = abi.window_config(B, Tq, Tk, Hq, Hkv, dqk, dv, W, ns, q0)
+    x = dict(q=r(B, Tq, Hq, dqk), k=r(B, Hkv, Tk, dqk), v=r(B, Hkv, Tk, dv))
+    return cfg, x, r(B, Tq, Hq, dv), visible(Tq, Tk, q0, W, ns, "cuda")
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_forward_and_backward(name):
+    cfg, x, d_out, vis = make(name)
+    out, lse = abi.window_forward(cfg, **x)
+    dq, dk, dv = abi.window_backward(cfg, **x, out=out, lse=lse, d_out=d_out)
+    torch.cuda.synchronize()
+    assert abi.nsa_get_device_status() == 0
+    ref = window_ref(x["q"], x["k"], x["v"], vis, cfg.scale, d_out)
+    for n, got in [("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)]:
+        check(got, ref[n], f"{name} {n}")
+
+
+@pytest.mark.parametrize("name", ["tiny", "gqa16_192", "sinks_meet_window"])
+def test_large_scores(name):
+    """Scores of several hundred: the running maximum moves often, weights underflow."""
+    cfg, x, d_out, vis = make(name, seed=1, spread=6.0)
+    out, lse = abi.window_forward(cfg, **x)
+    grads = abi.window_backward(cfg, **x, out=out, lse=lse, d_out=d_out)
+    ref = window_ref(x["q"], x["k"], x["v"], vis, cfg.scale, d_out)
+    for n, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse) + grads):
+        check(got, ref[n], f"{name} {n}")
+
+
+def test_lse_is_optional_and_calls_repeat_bit_for_bit():
+    cfg, x, d_out, _ = make("gqa16_192", seed=2)
+    out, lse = abi.window_forward(cfg, **x)
+    bare = torch.empty_like(out)
+    abi.nsa_window_attn_fwd(cfg, x["q"], x["k"], x["v"], bare)
+    first = abi.window_backward(cfg, **x, out=out, lse=lse, d_out=d_out)
+    second = abi.window_backward(cfg, **x, out=out, lse=lse, d_out=d_out)
+    assert torch.equal(out, bare)
+    for a, b in zip(first, second):
+        assert torch.equal(a, b)
+
+
+def test_no_queries():
+    cfg = abi.window_config(2, 0, 50, 4, 2, 64, 64, 8)
+    q = torch.empty(2, 0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.randn(2, 2, 50, 64, device="cuda").to(torch.bfloat16)
+    lse = torch.empty(2, 0, 4, device="cuda")
+    dk, dv = torch.full_like(k, 3.0), torch.full_like(k, 3.0)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    some = torch.empty(16, dtype=torch.bfloat16, device="cuda")       # an address for what has no element
+    abi.nsa_window_attn_fwd(cfg, some, k, k, some)
+    abi.nsa_window_attn_bwd(cfg, some, k, k, some, lse if lse.data_ptr() else some, some, some, dk, dv, ws, 256)
+    assert q.numel() == 0 and not dk.any() and not dv.any()
+
+
+def test_a_padded_batch_leaves_its_sequences_alone():
+    """Rows behind a sequence's end, with d_out = 0 there, change nothing before it."""
+    cfg, x, d_out, _ = make("mha", seed=3)
+    n = 211
+    d_out[:, n:] = 0
+    out, lse = abi.window_forward(cfg, **x)
+    dq, dk, dv = abi.window_backward(cfg, **x, out=out, lse=lse, d_out=d_out)
+    short = abi.window_config(2, n, n, 3, 3, 128, 128, 130, 16)
+    y = dict(q=x["q"][:, :n].contiguous(), k=x["k"][:, :, :n].contiguous(), v=x["v"][:, :, :n].contiguous())
+    vis = visible(n, n, 0, 130, 16, "cuda")
+    ref = window_ref(y["q"], y["k"], y["v"], vis, short.scale, d_out[:, :n])
+    check(out[:, :n], ref["out"], "out")
+    check(dq[:, :n], ref["dq"], "dq")
+    check(dk[:, :, :n], ref["dk"], "dk")
+    check(dv[:, :, :n], ref["dv"], "dv")
+    assert not dq[:, n:].any() and not dk[:, :, n:].any() and not dv[:, :, n:].any()
+
+
+def test_captured_and_on_a_side_stream():
+    cfg, x, d_out, vis = make("tiny", seed=4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, lse = abi.window_forward(cfg, **x)
+        abi.window_backward(cfg, **x, out=out, lse=lse, d_out=d_out)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g_out, g_lse = abi.window_forward(cfg, **x)
+        g_grads = abi.window_backward(cfg, **x, out=g_out, lse=g_lse, d_out=d_out)
+    fresh = make("tiny", seed=5)
+    for n in x:
+        x[n].copy_(fresh[1][n])
+    d_out.copy_(fresh[2])
+    graph.replay()
+    torch.cuda.synchronize()
+    ref = window_ref(x["q"], x["k"], x["v"], vis, cfg.scale, d_out)
+    for n, got in zip(("out", "lse", "dq", "dk", "dv"), (g_out, g_lse) + g_grads):
+        check(got, ref[n], n)
+
+
+def test_refuses_what_is_not_dense_or_of_another_type():
+    cfg, x, _, _ = make("tiny")
+    with pytest.raises(ValueError, match="contiguous"):
+        abi.window_forward(cfg, x["q"].transpose(1, 2).contiguous().transpose(1, 2), x["k"], x["v"])
+    with pytest.raises(ValueError, match="k is"):
+        abi.window_forward(cfg, x["q"], x["k"].float(), x["v"])
+    with pytest.raises(ValueError, match="one CUDA device"):
+        abi.window_forward(cfg, x["q"], x["k"], x["v"].cpu())
