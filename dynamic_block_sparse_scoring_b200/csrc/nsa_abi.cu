@@ -12,6 +12,7 @@
 #include <nvtx3/nvToolsExt.h>
 #include "abi_checks.cuh"
 #include "sel_index.cuh"
+#include "window.cuh"
 
 namespace {
 
@@ -678,8 +679,9 @@ nsa_status nsa_get_device_status(int32_t* status) {
     const int v3 = nsa::read_and_clear_dec_status();
     const int v4 = nsa::read_and_clear_select_status();
     const int v5 = nsa::read_and_clear_sctc_status();
-    if (v1 < 0 || v2 < 0 || v3 < 0 || v4 < 0 || v5 < 0) return NSA_ERR_CUDA;
-    *status = v1 ? v1 : (v2 ? v2 : (v3 ? v3 : (v4 ? v4 : v5)));
+    const int v6 = nsa::read_and_clear_win_fwd_status();
+    if (v1 < 0 || v2 < 0 || v3 < 0 || v4 < 0 || v5 < 0 || v6 < 0) return NSA_ERR_CUDA;
+    *status = v1 ? v1 : (v2 ? v2 : (v3 ? v3 : (v4 ? v4 : (v5 ? v5 : v6))));
     return NSA_OK;
 }
 

@@ -25,4 +25,10 @@ cudaError_t launch_window_rowwise_bwd(const WinShape& s, const __nv_bfloat16* q,
                                       const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
                                       const __nv_bfloat16* d_out, __nv_bfloat16* dq, __nv_bfloat16* dk,
                                       __nv_bfloat16* dv, float* delta, cudaStream_t st);
+
+// Tensor cores (window_fwd_tc.cu): d_qk <= 192, d_v <= 128, at most 64 heads per group.
+bool window_tc_supported(const WinShape& s);
+cudaError_t launch_window_fwd_tc(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                 const __nv_bfloat16* v, __nv_bfloat16* out, float* lse, cudaStream_t st);
+int read_and_clear_win_fwd_status();
 }  // namespace nsa

@@ -63,8 +63,10 @@ nsa_status nsa_window_attn_fwd(const nsa_window_config* cfg, const void* q, cons
     const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(q);
     const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(k);
     const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(v);
-    return cuda_status(nsa::launch_window_rowwise_fwd(s, qb, kb, vb, static_cast<__nv_bfloat16*>(out), lse,
-                                                      static_cast<cudaStream_t>(stream)));
+    __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(out);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (nsa::window_tc_supported(s)) return cuda_status(nsa::launch_window_fwd_tc(s, qb, kb, vb, ob, lse, cs));
+    return cuda_status(nsa::launch_window_rowwise_fwd(s, qb, kb, vb, ob, lse, cs));
 }
 
 nsa_status nsa_window_bwd_workspace_size(const nsa_window_config* cfg, size_t* bytes) {

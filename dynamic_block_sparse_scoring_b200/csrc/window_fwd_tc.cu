@@ -1,0 +1,500 @@
+// Sliding-window attention with sink tokens on the 5th-generation tensor cores
+// (tcgen05 + TMEM + TMA), forward.
+//
+// Transcript #94 (bidclub.ai) §4 (window and attention sink), §5 (the heads of
+// a group stacked as rows of one product with their shared keys).  With
+// s_u = scale q.k_u over the visible keys, x_u = s_u log2 e:
+//   S = Q K^T;  p_u = 2^(x_u - m), m a running reference of the row;
+//   O += P V;  l += sum p;  out = O / l;  lse = ln 2 (m + log2 l).
+// The reference moves only when the row's maximum passes it by more than 2^8
+// (any reference gives the same quotient; 2^8 keeps p far from overflow), so O
+// is rarely rescaled.  p enters P V rounded to bf16, l sums it unrounded.
+//
+// A query tile is 128 rows: 128 / G tokens (rounded down) x the G heads of a
+// KV head.  A CTA takes two neighbouring query tiles with the same keys and
+// walks their key tiles of 128: first the sinks' (when they lie before the
+// window), then the window's.  While one tile's softmax runs, the tensor
+// cores work for the other; the single issuing lane's order is
+//   S0(0) S1(0) | O0(0) S0(1) O1(0) S1(1) | O0(1) S0(2) O1(1) S1(2) | ...
+// As tcgen05 operations of one lane complete in order, S_t(j + 1) being there
+// means that O_t(j) is: the softmax may then rescale O and overwrite P without
+// another wait.
+//
+// Warps (384 threads): 0 loads Q and K, 1 issues the MMAs, 2 loads V, 3 idle;
+// 4-7 softmax and epilogue of tile 0, 8-11 of tile 1, one thread per row.
+// TMEM: S0, S1 (128 columns each, P over them as bf16), O0, O1 (d_v each).
+// Shared memory at d 192/128: Q 2 x 48 KB, K 2 x 48 KB, V 32 KB.
+// Bound by the tensor cores: a pair of tiles needs 2 x 128 x 128 x (d_qk + d_v)
+// MACs per key tile at 4096 a clock, its exponentials 2 x 16384 at 16 a clock.
+#include <math.h>
+
+#include <algorithm>
+
+#include "tc.cuh"
+#include "tmap.cuh"
+#include "window.cuh"
+
+namespace nsa {
+
+__device__ int g_win_fwd_status = 0;
+
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int CHUNK = 16384;                    // 128 rows x 64 columns of bf16
+constexpr int THREADS = 384;
+constexpr uint64_t WAIT_NS = 1000000000ull;
+
+template <int DQK, int DV>
+struct Smem {
+    static constexpr int QC = DQK / 64, VC = DV / 64;
+    static constexpr int KS = 2;
+    static constexpr int ROOM = 227 * 1024 - 1024 - 512 - (2 + KS) * QC * CHUNK;
+    static constexpr int VS = ROOM / (VC * CHUNK) >= 2 ? 2 : 1;
+    static constexpr int Q_OFF = 0;
+    static constexpr int K_OFF = 2 * QC * CHUNK;
+    static constexpr int V_OFF = K_OFF + KS * QC * CHUNK;
+    static constexpr int BAR_OFF = V_OFF + VS * VC * CHUNK;
+    static constexpr int ALLOC = BAR_OFF + 512 + 1024;      // slack to align the base to 1024 B
+};
+
+struct Bars {
+    uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+
+struct Args {
+    WinShape s;
+    __nv_bfloat16* out;
+    float* lse;
+    int tok;        // tokens per query tile
+    int n_tt;       // query tiles per (sequence, KV head)
+    int nt;         // query tiles per work item (1 or 2)
+    int n_work;
+    float scale_log2;
+};
+
+// One work item: query tiles tt0 .. tt0 + nt - 1 of one (sequence, KV head) and
+// the key tiles that any of them needs.
+struct Work {
+    int b, kvh, tt0, nt;
+    int pf[2], pl[2];   // first and last position of each query tile
+    int nst;            // key tiles of the sinks
+    int sl;             // sinks before the window: keys [0, sl)
+    int lo;             // first key of the window's tiles
+    int n;              // key tiles in all
+
+    __device__ __forceinline__ int key(int j) const { return j < nst ? j * BN : lo + (j - nst) * BN; }
+};
+
+__device__ __forceinline__ Work decode_work(const Args& a, int w) {
+    const WinShape& s = a.s;
+    const int planes = s.B * s.Hkv;
+    const int items = (a.n_tt + a.nt - 1) / a.nt;
+    Work k;
+    k.tt0 = (items - 1 - w / planes) * a.nt;    // the latest (with most keys) first
+    const int r = w % planes;
+    k.b = r / s.Hkv;
+    k.kvh = r % s.Hkv;
+    k.nt = min(a.nt, a.n_tt - k.tt0);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        k.pf[t] = s.q0 + (k.tt0 + t) * a.tok;
+        k.pl[t] = min(k.pf[t] + a.tok, s.q0 + s.Tq) - 1;
+    }
+    const int last = k.nt == 2 ? k.pl[1] : k.pl[0];
+    k.lo = max(0, k.pf[0] - s.win + 1);
+    k.sl = min(s.ns, k.lo);
+    k.nst = (k.sl + BN - 1) / BN;
+    if (k.lo < k.nst * BN) k.lo = k.sl = k.nst = 0;     // they meet: one range from 0
+    k.n = k.nst + (last - k.lo) / BN + 1;
+    return k;
+}
+
+// Some row of query tile t sees some key of key tile j.  (The selects keep the
+// work item in registers.)
+__device__ __forceinline__ bool needs(const WinShape& s, const Work& w, int t, int j) {
+    if (t >= w.nt) return false;
+    if (j < w.nst) return true;
+    const int u0 = w.key(j), pf = t ? w.pf[1] : w.pf[0], pl = t ? w.pl[1] : w.pl[0];
+    return u0 <= pl && (u0 + BN - 1 > pf - s.win || u0 < s.ns);
+}
+
+__device__ __forceinline__ int last_needed(const WinShape& s, const Work& w, int t) {
+    int j = w.n - 1;
+    while (j > 0 && !needs(s, w, t, j)) --j;
+    return j;
+}
+
+// Bits k of [0, 32 w + 32) in [lo, hi] for word w.
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
+    const int a = max(lo - 32 * w, 0), b = min(hi - 32 * w, 31);
+    if (b < a) return 0u;
+    return (0xFFFFFFFFu >> (31 - b)) & (0xFFFFFFFFu << a);
+}
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(THREADS, 1)
+    window_fwd_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v, const Args a) {
+    using L = Smem<DQK, DV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars& bar = *reinterpret_cast<Bars*>(sm + L::BAR_OFF);
+    volatile int* abort_flag = &bar.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WinShape& s = a.s;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bar.q_full[i], 1);
+            tc::mbar_init(&bar.q_empty[i], 1);
+            tc::mbar_init(&bar.k_full[i], 1);
+            tc::mbar_init(&bar.k_empty[i], 1);
+            tc::mbar_init(&bar.v_full[i], 1);
+            tc::mbar_init(&bar.v_empty[i], 1);
+            tc::mbar_init(&bar.s_full[i], 1);
+            tc::mbar_init(&bar.p_full[i], 4);
+            tc::mbar_init(&bar.o_full[i], 1);
+        }
+        tc::mbar_init(&bar.drain, 1);
+        bar.abort = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_map(&map_q);
+        tc::prefetch_map(&map_k);
+        tc::prefetch_map(&map_v);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&bar.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = bar.tmem;
+    auto wait = [&](uint64_t* b, uint32_t parity) { return tc::mbar_wait(b, parity, abort_flag, WAIT_NS); };
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        atomicExch(&g_win_fwd_status, (int)NSA_ERR_TIMEOUT);
+    };
+
+    if (warp < 4) {
+        // 4 x 32 x 88 + 8 x 32 x 208 = 64512, the 384 x 168 registers of the launch
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------ Q and K
+            uint32_t nq[2] = {0, 0}, nk = 0;
+            bool ok = true;
+            const uint32_t q_bytes = (uint32_t)(L::QC * a.tok * s.G * 128);
+            for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
+                const Work k = decode_work(a, w);
+                const int plane = k.b * s.Hkv + k.kvh;
+                for (int j = 0; ok && j < k.n; ++j) {
+                    const int st = nk % L::KS;
+                    if (j == 0) {
+                        // the first query tile goes before the first keys, the second behind them
+                        if (!wait(&bar.q_empty[0], (nq[0] & 1) ^ 1)) { ok = false; break; }
+                        tc::mbar_arrive_expect_tx(&bar.q_full[0], q_bytes);
+                        for (int c = 0; c < L::QC; ++c)
+                            tc::tma_load_4d(sm + L::Q_OFF + c * CHUNK, &map_q, &bar.q_full[0], 64 * c, k.kvh * s.G,
+                                            k.tt0 * a.tok, k.b);
+                        ++nq[0];
+                    }
+                    if (!wait(&bar.k_empty[st], ((nk / L::KS) & 1) ^ 1)) { ok = false; break; }
+                    tc::mbar_arrive_expect_tx(&bar.k_full[st], L::QC * CHUNK);
+                    for (int c = 0; c < L::QC; ++c)
+                        tc::tma_load_3d(sm + L::K_OFF + (st * L::QC + c) * CHUNK, &map_k, &bar.k_full[st], 64 * c,
+                                        k.key(j), plane);
+                    ++nk;
+                    if (j == 0 && k.nt == 2) {
+                        if (!wait(&bar.q_empty[1], (nq[1] & 1) ^ 1)) { ok = false; break; }
+                        tc::mbar_arrive_expect_tx(&bar.q_full[1], q_bytes);
+                        for (int c = 0; c < L::QC; ++c)
+                            tc::tma_load_4d(sm + L::Q_OFF + (L::QC + c) * CHUNK, &map_q, &bar.q_full[1], 64 * c,
+                                            k.kvh * s.G, (k.tt0 + 1) * a.tok, k.b);
+                        ++nq[1];
+                    }
+                }
+            }
+            if (!ok) give_up();
+            // every copy issued here has landed before the CTA ends
+            for (uint32_t i = 0; i < L::KS && i < nk; ++i) {
+                const uint32_t last = i + ((nk - 1 - i) / L::KS) * L::KS;
+                tc::mbar_wait_bounded(&bar.k_full[i], (last / L::KS) & 1, WAIT_NS);
+            }
+            for (int t = 0; t < 2; ++t)
+                if (nq[t] > 0) tc::mbar_wait_bounded(&bar.q_full[t], (nq[t] - 1) & 1, WAIT_NS);
+        } else if (warp == 2 && lane == 0) {
+            // ------------------------------------------------ V
+            uint32_t nv = 0;
+            bool ok = true;
+            for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
+                const Work k = decode_work(a, w);
+                const int plane = k.b * s.Hkv + k.kvh;
+                for (int j = 0; j < k.n; ++j) {
+                    const int st = nv % L::VS;
+                    if (!wait(&bar.v_empty[st], ((nv / L::VS) & 1) ^ 1)) { ok = false; break; }
+                    tc::mbar_arrive_expect_tx(&bar.v_full[st], L::VC * CHUNK);
+                    for (int c = 0; c < L::VC; ++c)
+                        tc::tma_load_3d(sm + L::V_OFF + (st * L::VC + c) * CHUNK, &map_v, &bar.v_full[st], 64 * c,
+                                        k.key(j), plane);
+                    ++nv;
+                }
+            }
+            if (!ok) give_up();
+            for (uint32_t i = 0; i < L::VS && i < nv; ++i) {
+                const uint32_t last = i + ((nv - 1 - i) / L::VS) * L::VS;
+                tc::mbar_wait_bounded(&bar.v_full[i], (last / L::VS) & 1, WAIT_NS);
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------ MMA issue
+            const uint32_t idesc_qk = tc::idesc_bf16_f32(BM, BN, false, false);
+            const uint32_t idesc_pv = tc::idesc_bf16_f32(BM, DV, false, true);
+            const uint32_t q_base = tc::smem_u32(sm + L::Q_OFF), k_base = tc::smem_u32(sm + L::K_OFF),
+                           v_base = tc::smem_u32(sm + L::V_OFF);
+            uint32_t nk = 0, nv = 0;            // key / value tiles of the works before this one
+            uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+            bool ok = true;
+            for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
+                const Work k = decode_work(a, w);
+                int pend[2] = {-1, -1};         // key tile whose P V is still to be issued
+                bool first[2] = {true, true};
+                const int jl[2] = {last_needed(s, k, 0), last_needed(s, k, 1)};
+                for (int j = 0; ok && j <= k.n; ++j) {
+                    bool have_k = false;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= k.nt) continue;
+                        const bool want = j < k.n && needs(s, k, t, j);
+                        if (pend[t] >= 0) {
+                            const int pj = pend[t];
+                            const uint32_t iv = nv + pj;
+                            if (!wait(&bar.p_full[t], np[t] & 1) ||
+                                !wait(&bar.v_full[iv % L::VS], (iv / L::VS) & 1)) { ok = false; break; }
+                            ++np[t];
+                            tc::fence_after_sync();
+                            const uint32_t vst = v_base + (iv % L::VS) * L::VC * CHUNK;
+#pragma unroll
+                            for (int kk = 0; kk < BN / 16; ++kk)
+                                tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
+                                           tc::sdesc_sw128(vst + kk * 2048, CHUNK, 1024), idesc_pv,
+                                           (first[t] && kk == 0) ? 0u : 1u);
+                            first[t] = false;
+                            if (t == 1 || k.nt == 1 || !needs(s, k, 1, pj)) tc::mma_commit(&bar.v_empty[iv % L::VS]);
+                            if (pj == jl[t]) tc::mma_commit(&bar.o_full[t]);
+                            pend[t] = -1;
+                        }
+                        if (want) {
+                            const uint32_t ik = nk + j;
+                            if (first[t] && !wait(&bar.q_full[t], nq[t] & 1)) { ok = false; break; }
+                            if (!have_k && !wait(&bar.k_full[ik % L::KS], (ik / L::KS) & 1)) { ok = false; break; }
+                            have_k = true;
+                            tc::fence_after_sync();
+                            const uint32_t kst = k_base + (ik % L::KS) * L::QC * CHUNK;
+#pragma unroll
+                            for (int kk = 0; kk < DQK / 16; ++kk) {
+                                const uint32_t off = (kk >> 2) * CHUNK + (kk & 3) * 32;
+                                tc::mma_ss(tmem + t * 128, tc::sdesc_sw128(q_base + t * L::QC * CHUNK + off, 16, 1024),
+                                           tc::sdesc_sw128(kst + off, 16, 1024), idesc_qk, kk > 0);
+                            }
+                            tc::mma_commit(&bar.s_full[t]);
+                            if (j == jl[t]) {
+                                tc::mma_commit(&bar.q_empty[t]);
+                                ++nq[t];
+                            }
+                            pend[t] = j;
+                        }
+                    }
+                    if (ok && j < k.n) {        // (every key tile has a query tile that needs it)
+                        if (!have_k && !wait(&bar.k_full[(nk + j) % L::KS], ((nk + j) / L::KS) & 1)) ok = false;
+                        if (ok) tc::mma_commit(&bar.k_empty[(nk + j) % L::KS]);
+                    }
+                }
+                nk += k.n;
+                nv += k.n;
+            }
+            if (!ok) give_up();
+            tc::mma_commit(&bar.drain);         // every MMA has completed before TMEM is freed
+            tc::mbar_wait_bounded(&bar.drain, 0, WAIT_NS);
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+        // ---------------------------------------------------- softmax and epilogue of one query tile
+        const int t = (warp - 4) >> 2;
+        const int r = (warp & 3) * 32 + lane;                   // row of the tile
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * DV + lane_off;
+        const int tt = r / s.G, g = r - tt * s.G;
+        uint32_t ns = 0, no = 0;
+        bool ok = true;
+        auto warp_wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
+        for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
+            const Work k = decode_work(a, w);
+            if (t >= k.nt) continue;
+            const int pos = (t == 0 ? k.pf[0] : k.pf[1]) + tt;
+            const bool row_ok = tt < a.tok && pos < s.q0 + s.Tq;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < k.n; ++j) {
+                if (!needs(s, k, t, j)) continue;
+                if (!warp_wait(&bar.s_full[t], ns & 1)) { ok = false; break; }
+                ++ns;
+                tc::fence_after_sync();
+                const int u0 = k.key(j);
+                // visible offsets: [lo, hi] and, behind the window, [0, sk)
+                int lo, hi, sk;
+                if (j < k.nst) {
+                    lo = 0;
+                    hi = k.sl - 1 - u0;
+                    sk = 0;
+                } else {
+                    lo = pos - s.win + 1 - u0;
+                    hi = pos - u0;
+                    sk = min(s.ns - u0, hi + 1);
+                }
+                uint32_t x[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + 32 * c, x + 32 * c);
+                tc::tmem_wait_ld();
+                const bool full = hi >= BN - 1 && (lo <= 0 || sk >= BN);
+                if (!__all_sync(0xffffffffu, full || !row_ok)) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t bits = range_bits(lo, hi, c) | range_bits(0, sk - 1, c);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((bits >> i) & 1u)) x[32 * c + i] = 0xFF800000u;
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+                // scale > 0, so the scaled maximum is the maximum of the scaled scores
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                float alpha = 1.f;
+                if (mt > m + 8.f || m == -INFINITY) {           // (-inf > -inf is false: m stays)
+                    if (m != -INFINITY) alpha = tc::ex2(m - mt);
+                    m = mt;
+                }
+                const float neg = m == -INFINITY ? 0.f : -m;
+                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 128; i += 2) {
+                    const float p0 = tc::ex2(fmaf(__uint_as_float(x[i]), a.scale_log2, neg));
+                    const float p1 = tc::ex2(fmaf(__uint_as_float(x[i + 1]), a.scale_log2, neg));
+                    ps[(i >> 1) & 3] += p0 + p1;
+                    x[i >> 1] = tc::pack_bf16x2(p0, p1);        // packed in place: i / 2 <= i
+                }
+                tc::tmem_st32(tS, x);
+                tc::tmem_st32(tS + 32, x + 32);
+                if (__any_sync(0xffffffffu, alpha != 1.f)) {    // O holds the tiles before this one
+#pragma unroll 1
+                    for (int c = 0; c < DV; c += 32) {
+                        uint32_t o[32];
+                        tc::tmem_ld32(tO + c, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tc::tmem_st32(tO + c, o);
+                    }
+                    l *= alpha;
+                }
+                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.p_full[t]);
+            }
+            if (!ok) break;
+            if (!warp_wait(&bar.o_full[t], no & 1)) { ok = false; break; }
+            ++no;
+            tc::fence_after_sync();
+            const size_t row = ((size_t)k.b * s.Tq + (pos - s.q0)) * s.Hq + k.kvh * s.G + g;
+            const float inv = 1.f / l;
+#pragma unroll 1
+            for (int c = 0; c < DV; c += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32(tO + c, o);
+                tc::tmem_wait_ld();
+                if (row_ok) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.out + row * DV + c);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float f[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[8 * q + e]) * inv;
+                        dst[q] = pack8(f);
+                    }
+                }
+            }
+            if (row_ok && a.lse) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+            tc::fence_before_sync();
+        }
+        if (!ok) give_up();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int DQK, int DV>
+cudaError_t launch_impl(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                        __nv_bfloat16* out, float* lse, cudaStream_t st) {
+    Args a;
+    a.s = s;
+    a.out = out;
+    a.lse = lse;
+    a.tok = BM / s.G;
+    a.n_tt = (s.Tq + a.tok - 1) / a.tok;
+    a.scale_log2 = s.scale * 1.4426950408889634f;
+    int dev = 0, nsm = 148;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long planes = (long long)s.B * s.Hkv;
+    // pairs of query tiles unless that would leave SMs without work
+    a.nt = (a.n_tt + 1) / 2 * planes >= nsm ? 2 : 1;
+    a.n_work = (int)((a.n_tt + a.nt - 1) / a.nt * planes);
+    CUtensorMap mq, mk, mv;
+    if (!tmap::heads_map(&mq, q, DQK, s.Hq, s.Tq, s.B, s.G, a.tok) ||
+        !tmap::rows_map(&mk, k, DQK, s.Tk, s.B * s.Hkv, BN) || !tmap::rows_map(&mv, v, DV, s.Tk, s.B * s.Hkv, BN))
+        return cudaErrorInvalidValue;
+    const int smem = Smem<DQK, DV>::ALLOC;
+    e = cudaFuncSetAttribute(window_fwd_tc_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    window_fwd_tc_kernel<DQK, DV><<<std::min(a.n_work, nsm), THREADS, smem, st>>>(mq, mk, mv, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool window_tc_supported(const WinShape& s) {
+    return s.dqk <= 192 && s.dv <= 128 && s.G <= 64;
+}
+
+cudaError_t launch_window_fwd_tc(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                 const __nv_bfloat16* v, __nv_bfloat16* out, float* lse, cudaStream_t st) {
+#define NSA_WIN_CASE(A, B) \
+    if (s.dqk == A && s.dv == B) return launch_impl<A, B>(s, q, k, v, out, lse, st);
+    NSA_WIN_CASE(64, 64)
+    NSA_WIN_CASE(64, 128)
+    NSA_WIN_CASE(128, 64)
+    NSA_WIN_CASE(128, 128)
+    NSA_WIN_CASE(192, 64)
+    NSA_WIN_CASE(192, 128)
+#undef NSA_WIN_CASE
+    return cudaErrorInvalidValue;
+}
+
+int read_and_clear_win_fwd_status() {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_win_fwd_status, sizeof(int)) != cudaSuccess) return -1;
+    cudaMemcpyToSymbol(g_win_fwd_status, &zero, sizeof(int));
+    return v;
+}
+
+}  // namespace nsa
