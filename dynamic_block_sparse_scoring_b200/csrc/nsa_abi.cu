@@ -680,8 +680,9 @@ nsa_status nsa_get_device_status(int32_t* status) {
     const int v4 = nsa::read_and_clear_select_status();
     const int v5 = nsa::read_and_clear_sctc_status();
     const int v6 = nsa::read_and_clear_win_fwd_status();
-    if (v1 < 0 || v2 < 0 || v3 < 0 || v4 < 0 || v5 < 0 || v6 < 0) return NSA_ERR_CUDA;
-    *status = v1 ? v1 : (v2 ? v2 : (v3 ? v3 : (v4 ? v4 : (v5 ? v5 : v6))));
+    const int v7 = nsa::read_and_clear_win_bwd_status();
+    if (v1 < 0 || v2 < 0 || v3 < 0 || v4 < 0 || v5 < 0 || v6 < 0 || v7 < 0) return NSA_ERR_CUDA;
+    *status = v1 ? v1 : (v2 ? v2 : (v3 ? v3 : (v4 ? v4 : (v5 ? v5 : (v6 ? v6 : v7)))));
     return NSA_OK;
 }
 

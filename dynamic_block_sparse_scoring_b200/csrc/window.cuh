@@ -31,4 +31,11 @@ bool window_tc_supported(const WinShape& s);
 cudaError_t launch_window_fwd_tc(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                  const __nv_bfloat16* v, __nv_bfloat16* out, float* lse, cudaStream_t st);
 int read_and_clear_win_fwd_status();
+// Backward for the same shapes (window_bwd_tc.cu); part: window_bwd_tc_part_bytes().
+size_t window_bwd_tc_part_bytes(const WinShape& s);
+cudaError_t launch_window_bwd_tc(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                 const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
+                                 const __nv_bfloat16* d_out, __nv_bfloat16* dq, __nv_bfloat16* dk,
+                                 __nv_bfloat16* dv, float* delta, float* part, cudaStream_t st);
+int read_and_clear_win_bwd_status();
 }  // namespace nsa

@@ -45,7 +45,12 @@ nsa_status make_win_shape(const nsa_window_config* cfg, WinShape* s) {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Workspace of the backward: delta [B, Tq, Hq], then the tensor-core kernel's partial sums.
 size_t delta_bytes(const WinShape& s) { return up256((size_t)s.B * s.Tq * s.Hq * 4); }
+
+size_t bwd_bytes(const WinShape& s) {
+    return delta_bytes(s) + (nsa::window_tc_supported(s) && s.Tq > 0 ? nsa::window_bwd_tc_part_bytes(s) : 0);
+}
 
 }  // namespace
 
@@ -74,7 +79,7 @@ nsa_status nsa_window_bwd_workspace_size(const nsa_window_config* cfg, size_t* b
     WinShape s;
     nsa_status st = make_win_shape(cfg, &s);
     if (st != NSA_OK) return st;
-    *bytes = delta_bytes(s);
+    *bytes = bwd_bytes(s);
     return NSA_OK;
 }
 
@@ -93,7 +98,14 @@ nsa_status nsa_window_attn_bwd(const nsa_window_config* cfg, const void* q, cons
         st = cuda_status(cudaMemsetAsync(dk, 0, (size_t)s.B * s.Hkv * s.Tk * s.dqk * 2, cs));
         return st != NSA_OK ? st : cuda_status(cudaMemsetAsync(dv, 0, (size_t)s.B * s.Hkv * s.Tk * s.dv * 2, cs));
     }
-    if (!workspace || ws_bytes < delta_bytes(s)) return NSA_ERR_WORKSPACE;
+    if (!workspace || ws_bytes < bwd_bytes(s)) return NSA_ERR_WORKSPACE;
+    if (nsa::window_tc_supported(s))
+        return cuda_status(nsa::launch_window_bwd_tc(
+            s, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
+            static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(out), lse,
+            static_cast<const __nv_bfloat16*>(d_out), static_cast<__nv_bfloat16*>(dq),
+            static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), static_cast<float*>(workspace),
+            reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + delta_bytes(s)), cs));
     return cuda_status(nsa::launch_window_rowwise_bwd(
         s, static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
         static_cast<const __nv_bfloat16*>(v), static_cast<const __nv_bfloat16*>(out), lse,

@@ -1,0 +1,740 @@
+// Sliding-window attention with sink tokens on the 5th-generation tensor cores
+// (tcgen05 + TMEM + TMA), backward.
+//
+// With x = log2 e (scale q.k - lse), p = 2^x (rebuilt from the forward's lse),
+// delta = do.o and ds = p (do.v - delta):
+//   dq = scale sum_u ds k_u,   dk_u = scale sum_t ds q_t,   dv_u = sum_t p do_t
+// (Transcript #94, bidclub.ai, §2 and §4: each output is a softmax-weighted sum
+// over the window and the sinks.)
+//
+// Two kernels of one shape.  128 rows stay resident, 64 rows at a time stream
+// past them, and every sum over the streamed side accumulates in TMEM:
+//             resident (M = 128)      streamed (N = 64)       accumulates
+//   DQ        Q, dO of a query tile   K, V of 64 keys         dQ += dS K
+//   DKV       K, V of a key tile      Q, dO of 64 query rows  dV += P dO, dK += dS Q
+// S = R1 T1^T and D = R2 T2^T are products of shared-memory operands, P and dS
+// (bf16, written over S in TMEM) are the A operand of the gradient products,
+// whose B is the streamed tile again, read MN-major.  So the scores are built
+// twice (seven products instead of five), but no gradient is added to memory:
+// no atomics, no fp32 dq in HBM, the same bits on every run.
+//
+// Queries are (token, head) rows of one KV head's group, so dk / dv sum over
+// the group in TMEM.  A key tile that many queries see (the sinks', or any on
+// a small problem) is cut into items over its queries, whose fp32 partial
+// sums window_bwd_join_kernel adds in order.
+//
+// Warps (384 threads): 0 TMA, 1 MMA issue (one lane), 2-3 the rows' (lse,
+// delta), 4-7 and 8-11 two warpgroups taking the steps in turn, one thread per
+// resident row.  The issue order S(i+1) D(i+1) | gradients(i) gives the softmax
+// of a step the tensor cores' time of a whole step.
+// Bound by the tensor cores and shared memory: a step (64 streamed rows) is
+// 128 x 64 x (2 d_qk + d_v) MACs in DQ, (2 d_qk + 2 d_v) in DKV, at 4096 a
+// clock; S and D (N = 64, both operands in shared memory) read 6 KB for 32
+// clocks of MMA, 1.5 times what shared memory gives.
+#include <math.h>
+
+#include <algorithm>
+
+#include "tc.cuh"
+#include "tmap.cuh"
+#include "window.cuh"
+
+namespace nsa {
+
+__device__ int g_win_bwd_status = 0;
+
+namespace {
+
+constexpr int BM = 128, BN = 64;
+constexpr int RCHUNK = 16384, TCHUNK = 8192;    // 128 / 64 rows x 64 columns of bf16
+constexpr int THREADS = 384;
+constexpr uint64_t WAIT_NS = 1000000000ull;
+constexpr int SMS = 148;                        // the split of key tiles is planned for this many SMs
+constexpr int MIN_CHUNK = 8;                    // least steps of an item of a split key tile
+constexpr float LOG2E = 1.4426950408889634f;
+
+enum { DQ = 0, DKV = 1 };
+
+template <int DQK, int DV, int MODE>
+struct Smem {
+    static constexpr int QC = DQK / 64, VC = DV / 64;
+    static constexpr int R_BYTES = (QC + VC) * RCHUNK, T_BYTES = (QC + VC) * TCHUNK;
+    static constexpr int NST = (216 * 1024 - R_BYTES) / T_BYTES >= 4 ? 4 : 3;
+    static constexpr int T_OFF = R_BYTES;
+    static constexpr int AUX_OFF = T_OFF + NST * T_BYTES;       // float2 (lse log2 e, delta)
+    static constexpr int AUX = MODE == DQ ? 2 * BM : NST * BN;  // two query tiles / one per stage
+    static constexpr int BAR_OFF = AUX_OFF + AUX * 8;
+    static constexpr int ALLOC = BAR_OFF + 512 + 1024;
+    static constexpr int ACC = MODE == DQ ? DQK : DQK + DV;     // accumulator columns
+    static constexpr int ND = 128 + 128 + ACC <= 512 ? 2 : 1;   // D buffers in TMEM
+    static constexpr int D_COL = 128, ACC_COL = 128 + 64 * ND;  // columns: S0 S1 | D .. | dQ  or  dV dK
+};
+
+struct Bars {
+    uint64_t r_full, r_empty, t_full[4], t_empty[4], s_full[2], d_full[2], d_read[2], p_full[2];
+    uint64_t acc_full, acc_free, aux_full[4], aux_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// How the key tiles are cut into items (DKV): key tiles below nsk hold sinks
+// and are seen by every later query, the others by the window's.
+struct Split {
+    int nk, nsk;        // key tiles, those with sinks
+    int chunk_s, chunk_o;   // steps per item
+    int sp_s, sp_o;     // most items of a key tile
+};
+
+struct Args {
+    WinShape s;
+    Split p;
+    const __nv_bfloat16* out;
+    const __nv_bfloat16* d_out;
+    const float* lse;
+    float* delta;
+    __nv_bfloat16* dq;
+    __nv_bfloat16* dk;
+    __nv_bfloat16* dv;
+    float* part;        // partial sums [slot][BM][DV + DQK]
+    int tok;            // tokens per query tile (DQ) or per step (DKV)
+    int n_tt;           // query tiles per (sequence, KV head) (DQ)
+    int n_work;
+    float scale_log2;
+};
+
+__host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Tokens [i0, i1) of the queries that see a key of the tile at u0.
+__host__ __device__ __forceinline__ void tile_queries(const WinShape& s, int u0, int* i0, int* i1) {
+    const long long last = u0 < s.ns ? (long long)s.q0 + s.Tq - 1
+                                     : min((long long)s.q0 + s.Tq - 1, (long long)u0 + BM - 1 + s.win - 1);
+    *i0 = max(u0, s.q0) - s.q0;
+    *i1 = max((int)(last + 1 - s.q0), *i0);
+}
+
+// One work item: the steps of a query tile (DQ) or of a share of a key tile's queries (DKV).
+struct Work {
+    int b, kvh, n;      // n: steps
+    int first;          // DQ: first token of the query tile.  DKV: first key of the tile
+    int base;           // DKV: token of step 0
+    int nst, sl, lo;    // DQ: sink steps, sinks before the window, first key of the window's steps
+    int slot;           // DKV: partial-sum slot, -1: the only item of its key tile
+};
+
+template <int MODE>
+__device__ __forceinline__ bool decode_work(const Args& a, int w, Work* k) {
+    const WinShape& s = a.s;
+    const int planes = s.B * s.Hkv;
+    if (MODE == DQ) {
+        const int r = w % planes, tt = a.n_tt - 1 - w / planes;     // the latest first
+        k->b = r / s.Hkv;
+        k->kvh = r % s.Hkv;
+        k->first = tt * a.tok;
+        const int pf = s.q0 + k->first, pl = min(pf + a.tok, s.q0 + s.Tq) - 1;
+        k->lo = max(0, pf - s.win + 1);
+        k->sl = min(s.ns, k->lo);
+        k->nst = ceil_div(k->sl, BN);
+        if (k->lo < k->nst * BN) k->lo = k->sl = k->nst = 0;        // they meet: one range from 0
+        k->n = k->nst + (pl - k->lo) / BN + 1;
+        return true;
+    }
+    const int n_s = planes * a.p.nsk * a.p.sp_s;
+    const bool sinks = w < n_s;
+    const int x = sinks ? w : w - n_s;
+    const int plane = x % planes, y = x / planes;
+    const int tiles = sinks ? a.p.nsk : a.p.nk - a.p.nsk;
+    const int kt = (sinks ? 0 : a.p.nsk) + y % tiles, c = y / tiles;
+    const int chunk = sinks ? a.p.chunk_s : a.p.chunk_o, sp = sinks ? a.p.sp_s : a.p.sp_o;
+    k->b = plane / s.Hkv;
+    k->kvh = plane % s.Hkv;
+    k->first = kt * BM;
+    int i0, i1;
+    tile_queries(s, k->first, &i0, &i1);
+    const int steps = ceil_div(i1 - i0, a.tok);
+    const int items = max(1, ceil_div(steps, chunk));
+    if (c >= items) return false;
+    k->base = i0 + c * chunk * a.tok;
+    k->n = min(chunk, steps - c * chunk);
+    k->slot = items == 1 ? -1
+                         : (sinks ? 0 : n_s) + (plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp + c;
+    return true;
+}
+
+// The w-th item of CTA c: items are dealt back and forth, heaviest first.
+__device__ __forceinline__ int dealt(int round) {
+    return round * (int)gridDim.x + ((round & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
+}
+
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
+    const int a = max(lo - 32 * w, 0), b = min(hi - 32 * w, 31);
+    if (b < a) return 0u;
+    return (0xFFFFFFFFu >> (31 - b)) & (0xFFFFFFFFu << a);
+}
+
+template <int DQK, int DV, int MODE>
+__global__ void __launch_bounds__(THREADS, 1)
+    window_bwd_tc_kernel(const __grid_constant__ CUtensorMap map_r1, const __grid_constant__ CUtensorMap map_r2,
+                         const __grid_constant__ CUtensorMap map_t1, const __grid_constant__ CUtensorMap map_t2,
+                         const Args a) {
+    using L = Smem<DQK, DV, MODE>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars& bar = *reinterpret_cast<Bars*>(sm + L::BAR_OFF);
+    float2* aux = reinterpret_cast<float2*>(sm + L::AUX_OFF);
+    volatile int* abort_flag = &bar.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const WinShape& s = a.s;
+
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&bar.r_full, 1);
+        tc::mbar_init(&bar.r_empty, 1);
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(&bar.t_full[i], 1);
+            tc::mbar_init(&bar.t_empty[i], 1);
+            tc::mbar_init(&bar.aux_full[i], MODE == DQ ? 2 : 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bar.s_full[i], 1);
+            tc::mbar_init(&bar.d_full[i], 1);
+            tc::mbar_init(&bar.d_read[i], 4);
+            tc::mbar_init(&bar.p_full[i], 4);
+            tc::mbar_init(&bar.aux_empty[i], 8);
+        }
+        tc::mbar_init(&bar.acc_full, 1);
+        tc::mbar_init(&bar.acc_free, 8);
+        tc::mbar_init(&bar.drain, 1);
+        bar.abort = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_map(&map_r1);
+        tc::prefetch_map(&map_r2);
+        tc::prefetch_map(&map_t1);
+        tc::prefetch_map(&map_t2);
+    }
+    if (MODE == DKV && a.tok * s.G < BN) {
+        // rows of a step that no query fills stay zero: they enter the sums over rows
+        for (int i = threadIdx.x; i < L::NST * L::T_BYTES / 16; i += THREADS)
+            reinterpret_cast<uint4*>(sm + L::T_OFF)[i] = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&bar.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = bar.tmem;
+    auto wait = [&](uint64_t* b, uint32_t parity) { return tc::mbar_wait(b, parity, abort_flag, WAIT_NS); };
+    auto warp_wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        atomicExch(&g_win_bwd_status, (int)NSA_ERR_TIMEOUT);
+    };
+
+    if (warp < 4) {
+        // 4 x 32 x 88 + 8 x 32 x 208 = 64512, the 384 x 168 registers of the launch
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------ copies
+            uint32_t nr = 0, g = 0;
+            bool ok = true;
+            const int rows = a.tok * s.G;
+            const uint32_t r_bytes = (L::QC + L::VC) * (MODE == DQ ? rows * 128 : RCHUNK);
+            const uint32_t t_bytes = (L::QC + L::VC) * (MODE == DQ ? TCHUNK : rows * 128);
+            for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
+                Work k;
+                if (!decode_work<MODE>(a, w, &k) || k.n == 0) continue;
+                const int plane = k.b * s.Hkv + k.kvh, h0 = k.kvh * s.G;
+                if (!wait(&bar.r_empty, (nr & 1) ^ 1)) { ok = false; break; }
+                tc::mbar_arrive_expect_tx(&bar.r_full, r_bytes);
+#pragma unroll
+                for (int c = 0; c < L::QC + L::VC; ++c) {
+                    const CUtensorMap* m = c < L::QC ? &map_r1 : &map_r2;
+                    const int x = 64 * (c < L::QC ? c : c - L::QC);
+                    if (MODE == DQ) tc::tma_load_4d(sm + c * RCHUNK, m, &bar.r_full, x, h0, k.first, k.b);
+                    else tc::tma_load_3d(sm + c * RCHUNK, m, &bar.r_full, x, k.first, plane);
+                }
+                ++nr;
+                for (int i = 0; i < k.n; ++i, ++g) {
+                    const int st = g % L::NST;
+                    if (!wait(&bar.t_empty[st], ((g / L::NST) & 1) ^ 1)) { ok = false; break; }
+                    tc::mbar_arrive_expect_tx(&bar.t_full[st], t_bytes);
+                    uint8_t* dst = sm + L::T_OFF + st * L::T_BYTES;
+#pragma unroll
+                    for (int c = 0; c < L::QC + L::VC; ++c) {
+                        const CUtensorMap* m = c < L::QC ? &map_t1 : &map_t2;
+                        const int x = 64 * (c < L::QC ? c : c - L::QC);
+                        if (MODE == DQ)
+                            tc::tma_load_3d(dst + c * TCHUNK, m, &bar.t_full[st], x,
+                                            i < k.nst ? i * BN : k.lo + (i - k.nst) * BN, plane);
+                        else
+                            tc::tma_load_4d(dst + c * TCHUNK, m, &bar.t_full[st], x, h0, k.base + i * a.tok, k.b);
+                    }
+                }
+            }
+            if (!ok) give_up();
+            // every copy issued here has landed before the CTA ends
+            for (uint32_t i = 0; i < L::NST && i < g; ++i) {
+                const uint32_t last = i + ((g - 1 - i) / L::NST) * L::NST;
+                tc::mbar_wait_bounded(&bar.t_full[i], (last / L::NST) & 1, WAIT_NS);
+            }
+            if (nr > 0) tc::mbar_wait_bounded(&bar.r_full, (nr - 1) & 1, WAIT_NS);
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------ MMA issue
+            const uint32_t idesc_sd = tc::idesc_bf16_f32(BM, BN, false, false);
+            const uint32_t idesc_q = tc::idesc_bf16_f32(BM, DQK, false, true);
+            const uint32_t idesc_v = tc::idesc_bf16_f32(BM, DV, false, true);
+            const uint32_t r_base = tc::smem_u32(sm), t_base = tc::smem_u32(sm + L::T_OFF);
+            uint32_t g = 0, works = 0;          // steps and works before this work
+            bool ok = true;
+            auto scores = [&](uint32_t e) {     // S and D of step e
+                const int st = e % L::NST, b = e & 1;
+                if (!wait(&bar.t_full[st], (e / L::NST) & 1)) return false;
+                tc::fence_after_sync();
+                const uint32_t t0 = t_base + st * L::T_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < DQK / 16; ++kk)
+                    tc::mma_ss(tmem + b * 64, tc::sdesc_sw128(r_base + (kk >> 2) * RCHUNK + (kk & 3) * 32, 16, 1024),
+                               tc::sdesc_sw128(t0 + (kk >> 2) * TCHUNK + (kk & 3) * 32, 16, 1024), idesc_sd, kk > 0);
+                tc::mma_commit(&bar.s_full[b]);
+                // one D buffer: the step before this one must have read it
+                if (L::ND == 1 && e > 0 && !wait(&bar.d_read[b ^ 1], ((e - 1) >> 1) & 1)) return false;
+                tc::fence_after_sync();
+                const uint32_t tD = tmem + L::D_COL + (L::ND == 2 ? b * 64 : 0);
+#pragma unroll
+                for (int kk = 0; kk < DV / 16; ++kk)
+                    tc::mma_ss(tD, tc::sdesc_sw128(r_base + (L::QC + (kk >> 2)) * RCHUNK + (kk & 3) * 32, 16, 1024),
+                               tc::sdesc_sw128(t0 + (L::QC + (kk >> 2)) * TCHUNK + (kk & 3) * 32, 16, 1024), idesc_sd,
+                               kk > 0);
+                tc::mma_commit(&bar.d_full[b]);
+                return true;
+            };
+            for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
+                Work k;
+                if (!decode_work<MODE>(a, w, &k) || k.n == 0) continue;
+                if (!wait(&bar.r_full, works & 1) || !scores(g)) { ok = false; break; }
+                for (int i = 0; i < k.n; ++i, ++g) {
+                    if (i + 1 < k.n && !scores(g + 1)) { ok = false; break; }
+                    if (i + 1 == k.n) tc::mma_commit(&bar.r_empty);     // the residents' last use
+                    const int st = g % L::NST, b = g & 1;
+                    if (!wait(&bar.p_full[b], (g >> 1) & 1)) { ok = false; break; }
+                    if (i == 0 && !wait(&bar.acc_free, (works & 1) ^ 1)) { ok = false; break; }
+                    tc::fence_after_sync();
+                    const uint32_t t0 = t_base + st * L::T_BYTES, tA = tmem + b * 64, tG = tmem + L::ACC_COL;
+                    if (MODE == DKV) {
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            tc::mma_ts(tG, tA + kk * 8, tc::sdesc_sw128(t0 + L::QC * TCHUNK + kk * 2048, TCHUNK, 1024),
+                                       idesc_v, (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    const uint32_t tGq = MODE == DKV ? tG + DV : tG, tAq = MODE == DKV ? tA + 32 : tA;
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        tc::mma_ts(tGq, tAq + kk * 8, tc::sdesc_sw128(t0 + kk * 2048, TCHUNK, 1024), idesc_q,
+                                   (i > 0 || kk > 0) ? 1u : 0u);
+                    tc::mma_commit(&bar.t_empty[st]);
+                }
+                if (ok) tc::mma_commit(&bar.acc_full);
+                ++works;
+            }
+            if (!ok) give_up();
+            tc::mma_commit(&bar.drain);         // every MMA has completed before TMEM is freed
+            tc::mbar_wait_bounded(&bar.drain, 0, WAIT_NS);
+        } else if (MODE == DQ && warp >= 2) {
+            // ------------------------------------------------ (lse, delta) of a query tile's rows
+            // LPR lanes hold a row's d_v values, 16 bytes each; warps 2 and 3 take half of the rows
+            constexpr int LPR = DV / 8, RPI = 32 / LPR, U = 4;
+            const int half = (warp - 2) * (BM / 2), sub = lane / LPR, col = (lane % LPR) * 8;
+            uint32_t n = 0;
+            bool ok = true;
+            for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round, ++n) {
+                Work k;
+                decode_work<MODE>(a, w, &k);
+                const int buf = n & 1;
+                if (!warp_wait(&bar.aux_empty[buf], ((n >> 1) & 1) ^ 1)) { ok = false; break; }
+                for (int r0 = half; r0 < half + BM / 2; r0 += RPI * U) {
+                    uint4 x[U], y[U];
+                    float ls[U];
+                    long long row[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int r = r0 + u * RPI + sub, tt = r / s.G, i = k.first + tt;
+                        row[u] = tt < a.tok && i < s.Tq
+                                     ? ((long long)k.b * s.Tq + i) * s.Hq + k.kvh * s.G + (r - tt * s.G)
+                                     : -1;
+                        x[u] = y[u] = make_uint4(0, 0, 0, 0);
+                        ls[u] = INFINITY;
+                        if (row[u] >= 0) {
+                            x[u] = *reinterpret_cast<const uint4*>(a.out + row[u] * DV + col);
+                            y[u] = *reinterpret_cast<const uint4*>(a.d_out + row[u] * DV + col);
+                            ls[u] = a.lse[row[u]];
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        float f[8], h[8], d = 0.f;
+                        unpack8(x[u], f);
+                        unpack8(y[u], h);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) d = fmaf(f[e], h[e], d);
+#pragma unroll
+                        for (int o = LPR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+                        if (lane % LPR == 0) {
+                            aux[buf * BM + r0 + u * RPI + sub] = make_float2(ls[u] * LOG2E, d);
+                            if (row[u] >= 0) a.delta[row[u]] = d;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.aux_full[buf]);
+            }
+            if (!ok) give_up();
+        } else if (MODE == DKV && warp == 2) {
+            // ------------------------------------------------ (lse, delta) of a step's rows
+            uint32_t g = 0;
+            bool ok = true;
+            for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
+                Work k;
+                if (!decode_work<MODE>(a, w, &k) || k.n == 0) continue;
+                for (int i = 0; i < k.n; ++i, ++g) {
+                    const int st = g % L::NST;
+                    float2 v[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = lane + 32 * e, tt = r / s.G, tok = k.base + i * a.tok + tt;
+                        v[e] = make_float2(INFINITY, 0.f);      // p = 0: no query
+                        if (tt < a.tok && tok < s.Tq) {
+                            const size_t row = ((size_t)k.b * s.Tq + tok) * s.Hq + k.kvh * s.G + (r - tt * s.G);
+                            v[e] = make_float2(a.lse[row] * LOG2E, a.delta[row]);
+                        }
+                    }
+                    if (!warp_wait(&bar.t_empty[st], ((g / L::NST) & 1) ^ 1)) { ok = false; break; }
+                    aux[st * BN + lane] = v[0];
+                    aux[st * BN + lane + 32] = v[1];
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.aux_full[st]);
+                }
+            }
+            if (!ok) give_up();
+        }
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+        // ---------------------------------------------------- P and dS of every second step, gradients out
+        const int wg = (warp - 4) >> 2;
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + wg * 64 + lane_off;
+        const uint32_t tD = tmem + L::D_COL + (L::ND == 2 ? wg * 64 : 0) + lane_off;
+        const uint32_t tG = tmem + L::ACC_COL + lane_off;
+        const int tt = r / s.G, gh = r - tt * s.G;
+        uint32_t g = 0, works = 0, n = 0;
+        bool ok = true;
+        for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
+            Work k;
+            if (!decode_work<MODE>(a, w, &k)) continue;
+            float2 mine = make_float2(0.f, 0.f);
+            const int pos = MODE == DQ ? s.q0 + k.first + tt : k.first + r;     // query position or key
+            if (MODE == DQ) {
+                const int buf = n & 1;
+                if (!warp_wait(&bar.aux_full[buf], (n >> 1) & 1)) { ok = false; break; }
+                mine = aux[buf * BM + r];
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.aux_empty[buf]);
+                ++n;
+            }
+            for (int i = 0; i < k.n; ++i, ++g) {
+                if ((int)(g & 1) != wg) continue;
+                if (!warp_wait(&bar.s_full[wg], (g >> 1) & 1)) { ok = false; break; }
+                const int st = g % L::NST;
+                if (MODE == DKV && !warp_wait(&bar.aux_full[st], (g / L::NST) & 1)) { ok = false; break; }
+                tc::fence_after_sync();
+                uint32_t x[64], y[64];
+                tc::tmem_ld32(tS, x);
+                tc::tmem_ld32(tS + 32, x + 32);
+                // visible columns [lo, hi] and [0, sk)
+                int lo, hi, sk = 0;
+                if (MODE == DQ) {
+                    const int u0 = i < k.nst ? i * BN : k.lo + (i - k.nst) * BN;
+                    if (i < k.nst) {
+                        lo = 0;
+                        hi = k.sl - 1 - u0;
+                    } else {
+                        lo = pos - s.win + 1 - u0;
+                        hi = pos - u0;
+                        sk = min(s.ns - u0, hi + 1);
+                    }
+                } else {
+                    // tokens from pos on, up to pos + win - 1 unless the key is a sink
+                    const int tb = s.q0 + k.base + i * a.tok;
+                    lo = max(min(pos - tb, BN), -BN) * s.G;
+                    hi = pos < s.ns ? BN - 1 : max(min(pos - tb + s.win, BN), -BN) * s.G - 1;
+                }
+                const float4* ax = reinterpret_cast<const float4*>(aux + st * BN);      // DKV: two columns each
+                tc::tmem_wait_ld();
+                const bool full = hi >= BN - 1 && (lo <= 0 || sk >= BN);
+                if (!__all_sync(0xffffffffu, full)) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t bits = range_bits(lo, hi, c) | range_bits(0, sk - 1, c);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) x[32 * c + e] = 0xFF800000u;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                    float l0 = mine.x, l1 = mine.x;
+                    if (MODE == DKV) {
+                        const float4 v = ax[c / 2];
+                        l0 = v.x;
+                        l1 = v.z;
+                    }
+                    x[c] = __float_as_uint(tc::ex2(fmaf(__uint_as_float(x[c]), a.scale_log2, -l0)));
+                    x[c + 1] = __float_as_uint(tc::ex2(fmaf(__uint_as_float(x[c + 1]), a.scale_log2, -l1)));
+                }
+                if (!warp_wait(&bar.d_full[wg], (g >> 1) & 1)) { ok = false; break; }
+                tc::fence_after_sync();
+                tc::tmem_ld32(tD, y);
+                tc::tmem_ld32(tD + 32, y + 32);
+                tc::tmem_wait_ld();
+                if (L::ND == 1) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.d_read[wg]);
+                }
+                // bf16 weights and ds: half a step, 2^-9 relative of each term
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                    float e0 = mine.y, e1 = mine.y;
+                    if (MODE == DKV) {
+                        const float4 v = ax[c / 2];
+                        e0 = v.y;
+                        e1 = v.w;
+                    }
+                    const float p0 = __uint_as_float(x[c]), p1 = __uint_as_float(x[c + 1]);
+                    y[c / 2] = tc::pack_bf16x2(p0 * (__uint_as_float(y[c]) - e0), p1 * (__uint_as_float(y[c + 1]) - e1));
+                    x[c / 2] = tc::pack_bf16x2(p0, p1);
+                }
+                if (MODE == DKV) {
+                    tc::tmem_st32(tS, x);
+                    tc::tmem_st32(tS + 32, y);
+                } else {
+                    tc::tmem_st32(tS, y);
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.p_full[wg]);
+            }
+            if (!ok) break;
+            if (k.n > 0) {
+                if (!warp_wait(&bar.acc_full, works & 1)) { ok = false; break; }
+                tc::fence_after_sync();
+            }
+            // this warpgroup's 32-column pieces of the accumulator row
+            size_t qrow = 0;
+            bool row_ok;
+            if (MODE == DQ) {
+                row_ok = tt < a.tok && k.first + tt < s.Tq;
+                qrow = ((size_t)k.b * s.Tq + k.first + tt) * s.Hq + k.kvh * s.G + gh;
+            } else {
+                row_ok = pos < s.Tk;
+                qrow = ((size_t)k.b * s.Hkv + k.kvh) * s.Tk + pos;
+            }
+#pragma unroll 1
+            for (int c = wg * 32; c < L::ACC; c += 64) {
+                uint32_t o[32];
+                if (k.n > 0) {
+                    tc::tmem_ld32(tG + c, o);
+                    tc::tmem_wait_ld();
+                } else {                            // keys that no query sees
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+                if (row_ok && MODE == DKV && k.slot >= 0) {
+                    float4* dst = reinterpret_cast<float4*>(a.part + ((size_t)k.slot * BM + r) * L::ACC + c);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                             __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+                } else if (row_ok) {
+                    const bool val = MODE == DKV && c < DV;
+                    const float f = val ? 1.f : s.scale;
+                    __nv_bfloat16* row = MODE == DQ ? a.dq + qrow * DQK + c
+                                         : val      ? a.dv + qrow * DV + c
+                                                    : a.dk + qrow * DQK + (c - DV);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float z[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(o[8 * q + e]) * f;
+                        reinterpret_cast<uint4*>(row)[q] = pack8(z);
+                    }
+                }
+                __syncwarp();
+            }
+            if (k.n > 0) {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.acc_free);
+                ++works;
+            }
+        }
+        if (!ok) give_up();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+// Adds the items' partial sums of a split key tile, in order: one thread per
+// (row, four columns), JROWS rows per CTA.
+constexpr int JROWS = 4;
+
+template <int DQK, int DV>
+__global__ void __launch_bounds__(JROWS*(DQK + DV) / 4) window_bwd_join_kernel(const Args a) {
+    constexpr int C4 = (DQK + DV) / 4;
+    const WinShape& s = a.s;
+    const int planes = s.B * s.Hkv;
+    const int n_s = planes * a.p.nsk * a.p.sp_s;
+    const int plane = blockIdx.x % planes, kt = blockIdx.x / planes;
+    const bool sinks = kt < a.p.nsk;
+    int i0, i1;
+    tile_queries(s, kt * BM, &i0, &i1);
+    const int items = ceil_div(ceil_div(i1 - i0, a.tok), sinks ? a.p.chunk_s : a.p.chunk_o);
+    if (items <= 1) return;
+    const int tiles = sinks ? a.p.nsk : a.p.nk - a.p.nsk, sp = sinks ? a.p.sp_s : a.p.sp_o;
+    const size_t slot = (sinks ? 0 : n_s) + (size_t)(plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp;
+    const int r = blockIdx.y * JROWS + threadIdx.x / C4, c = (threadIdx.x % C4) * 4;
+    const int u = kt * BM + r;
+    if (u >= s.Tk) return;
+    const float4* src = reinterpret_cast<const float4*>(a.part + (slot * BM + r) * (DQK + DV) + c);
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = 0; i < items; ++i) {
+        const float4 x = src[(size_t)i * BM * C4];
+        t = make_float4(t.x + x.x, t.y + x.y, t.z + x.z, t.w + x.w);
+    }
+    const size_t row = (size_t)plane * s.Tk + u;
+    const float f = c < DV ? 1.f : s.scale;
+    __nv_bfloat16* dst = c < DV ? a.dv + row * DV + c : a.dk + row * DQK + (c - DV);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(tc::pack_bf16x2(t.x * f, t.y * f), tc::pack_bf16x2(t.z * f, t.w * f));
+}
+
+Split make_split(const WinShape& s) {
+    Split p;
+    const int tok = BN / s.G;
+    const long long planes = (long long)s.B * s.Hkv;
+    p.nk = ceil_div(s.Tk, BM);
+    p.nsk = ceil_div(s.ns, BM);
+    const int n_s = ceil_div(s.Tq, tok);                        // steps of a key tile that every query sees
+    const int n_o = std::min(n_s, (int)(((long long)BM + s.win + tok - 2) / tok));     // of one the window sees
+    const int others = p.nk - p.nsk;
+    const long long total = planes * ((long long)p.nsk * n_s + (long long)others * n_o);
+    // items of about half an SM's share; whole key tiles where there are enough of them
+    const int half = (int)std::min<long long>(std::max<long long>((total / SMS + 1) / 2, MIN_CHUNK), INT32_MAX);
+    p.chunk_s = std::max(1, std::min(half, n_s));
+    p.chunk_o = std::max(1, planes * others >= 2 * SMS ? n_o : std::min(half, n_o));
+    p.sp_s = ceil_div(n_s, p.chunk_s);
+    p.sp_o = ceil_div(n_o, p.chunk_o);
+    return p;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t part_slots(const WinShape& s, const Split& p) {
+    return (size_t)s.B * s.Hkv * ((size_t)p.nsk * p.sp_s + (p.sp_o > 1 ? (size_t)(p.nk - p.nsk) * p.sp_o : 0));
+}
+
+template <int DQK, int DV>
+cudaError_t launch_impl(Args a, const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                        cudaStream_t st) {
+    const WinShape& s = a.s;
+    const int planes = s.B * s.Hkv;
+    int dev = 0, nsm = 148;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int tok_q = BM / s.G, tok_s = BN / s.G;
+    CUtensorMap q128, do128, k64, v64, k128, v128, q64, do64;
+    if (!tmap::heads_map(&q128, q, DQK, s.Hq, s.Tq, s.B, s.G, tok_q) ||
+        !tmap::heads_map(&do128, a.d_out, DV, s.Hq, s.Tq, s.B, s.G, tok_q) ||
+        !tmap::heads_map(&q64, q, DQK, s.Hq, s.Tq, s.B, s.G, tok_s) ||
+        !tmap::heads_map(&do64, a.d_out, DV, s.Hq, s.Tq, s.B, s.G, tok_s) ||
+        !tmap::rows_map(&k64, k, DQK, s.Tk, planes, BN) || !tmap::rows_map(&v64, v, DV, s.Tk, planes, BN) ||
+        !tmap::rows_map(&k128, k, DQK, s.Tk, planes, BM) || !tmap::rows_map(&v128, v, DV, s.Tk, planes, BM))
+        return cudaErrorInvalidValue;
+    {
+        using L = Smem<DQK, DV, DQ>;
+        auto kernel = window_bwd_tc_kernel<DQK, DV, DQ>;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+        if (e != cudaSuccess) return e;
+        a.tok = tok_q;
+        a.n_tt = ceil_div(s.Tq, tok_q);
+        a.n_work = a.n_tt * planes;
+        kernel<<<std::min(a.n_work, nsm), THREADS, L::ALLOC, st>>>(q128, do128, k64, v64, a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    using L = Smem<DQK, DV, DKV>;
+    auto kernel = window_bwd_tc_kernel<DQK, DV, DKV>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    a.tok = tok_s;
+    a.n_work = planes * (a.p.nsk * a.p.sp_s + (a.p.nk - a.p.nsk) * a.p.sp_o);
+    kernel<<<std::min(a.n_work, nsm), THREADS, L::ALLOC, st>>>(k128, v128, q64, do64, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || (a.p.sp_s <= 1 && a.p.sp_o <= 1)) return e;
+    const int tiles = a.p.sp_o > 1 ? a.p.nk : a.p.nsk;
+    window_bwd_join_kernel<DQK, DV>
+        <<<dim3(tiles * planes, BM / JROWS), JROWS * (DQK + DV) / 4, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t window_bwd_tc_part_bytes(const WinShape& s) {
+    const Split p = make_split(s);
+    return up256(part_slots(s, p) * BM * (s.dqk + s.dv) * 4);
+}
+
+cudaError_t launch_window_bwd_tc(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
+                                 const __nv_bfloat16* v, const __nv_bfloat16* out, const float* lse,
+                                 const __nv_bfloat16* d_out, __nv_bfloat16* dq, __nv_bfloat16* dk,
+                                 __nv_bfloat16* dv, float* delta, float* part, cudaStream_t st) {
+    Args a;
+    a.s = s;
+    a.p = make_split(s);
+    a.out = out;
+    a.d_out = d_out;
+    a.lse = lse;
+    a.delta = delta;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.part = part;
+    a.tok = a.n_tt = a.n_work = 0;
+    a.scale_log2 = s.scale * LOG2E;
+#define NSA_WIN_CASE(A, B) \
+    if (s.dqk == A && s.dv == B) return launch_impl<A, B>(a, q, k, v, st);
+    NSA_WIN_CASE(64, 64)
+    NSA_WIN_CASE(64, 128)
+    NSA_WIN_CASE(128, 64)
+    NSA_WIN_CASE(128, 128)
+    NSA_WIN_CASE(192, 64)
+    NSA_WIN_CASE(192, 128)
+#undef NSA_WIN_CASE
+    return cudaErrorInvalidValue;
+}
+
+int read_and_clear_win_bwd_status() {
+    int v = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&v, g_win_bwd_status, sizeof(int)) != cudaSuccess) return -1;
+    cudaMemcpyToSymbol(g_win_bwd_status, &zero, sizeof(int));
+    return v;
+}
+
+}  // namespace nsa
