@@ -415,31 +415,52 @@ def nsa_pages_compact(cfg, k_pages, v_pages, table, lens, ref, remap, n_live, wo
                                  _ptr(workspace), ws_bytes, _stream(stream)))
 
 
-def _on(*named):
-    """Checks (name, tensor, shape, dtype) tuples: dense tensors of one CUDA device, which becomes
-    the current one inside the returned context."""
+def _device(*named):
+    """Checks (name, tensor, shape, dtype) tuples: dense tensors of one CUDA device, returned."""
     dev = named[0][1].device
+    if dev.type != "cuda":
+        raise ValueError(f"{named[0][0]} is on {dev}: all tensors belong on one CUDA device")
     for name, t, shape, dtype in named:
-        if t.device != dev or dev.type != "cuda":
+        if t.device != dev:
             raise ValueError(f"{name} is on {t.device}: all tensors belong on one CUDA device")
         if t.dtype != dtype or t.shape != shape:
             raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}: expected {dtype} {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} is not contiguous")
-    return torch.cuda.device(dev)
+    return dev
 
 
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+def _run(fn, dev, cfg, *args):
+    """Calls an entry point with cfg, the given tensors, sizes and Nones, and dev's current stream;
+    dev becomes the current device for the call where it is not."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _run(fn, dev, cfg, *args)
+    status = getattr(lib, fn)(cfg, *[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args],
+                              torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != 0:
+        raise NsaError(fn, status)
+
+
+def _size(fn, cfg) -> int:
+    n = _sz(0)
+    status = getattr(lib, fn)(cfg, n)
+    if status != 0:
+        raise NsaError(fn, status)
+    return n.value
+
+
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def window_forward(cfg: NsaWindowConfig, q, k, v):
     """Window attention with sink tokens on the current stream: (out bf16, lse fp32)."""
     B, Tq, Hq, Tk = cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.seqlen_kv
-    with _on(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), ("k", k, (B, cfg.h_kv, Tk, cfg.d_qk), _BF16),
-             ("v", v, (B, cfg.h_kv, Tk, cfg.d_v), _BF16)):
-        out = torch.empty(B, Tq, Hq, cfg.d_v, dtype=_BF16, device=q.device)
-        lse = torch.empty(B, Tq, Hq, dtype=_F32, device=q.device)
-        nsa_window_attn_fwd(cfg, q, k, v, out, lse)
+    dev = _device(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), ("k", k, (B, cfg.h_kv, Tk, cfg.d_qk), _BF16),
+                  ("v", v, (B, cfg.h_kv, Tk, cfg.d_v), _BF16))
+    out = torch.empty((B, Tq, Hq, cfg.d_v), dtype=_BF16, device=dev)
+    lse = torch.empty((B, Tq, Hq), dtype=_F32, device=dev)
+    _run("nsa_window_attn_fwd", dev, cfg, q, k, v, out, lse)
     return out, lse
 
 
@@ -447,12 +468,13 @@ def window_backward(cfg: NsaWindowConfig, q, k, v, out, lse, d_out):
     """Gradients (dq, dk, dv), bf16, of window_forward on the current stream."""
     B, Tq, Hq, Tk = cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.seqlen_kv
     o_shape = (B, Tq, Hq, cfg.d_v)
-    with _on(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), ("k", k, (B, cfg.h_kv, Tk, cfg.d_qk), _BF16),
-             ("v", v, (B, cfg.h_kv, Tk, cfg.d_v), _BF16), ("out", out, o_shape, _BF16),
-             ("lse", lse, (B, Tq, Hq), _F32), ("d_out", d_out, o_shape, _BF16)):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws = torch.empty(nsa_window_bwd_workspace_size(cfg), dtype=torch.uint8, device=q.device)
-        nsa_window_attn_bwd(cfg, q, k, v, out, lse, d_out, dq, dk, dv, ws, ws.numel())
+    dev = _device(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), ("k", k, (B, cfg.h_kv, Tk, cfg.d_qk), _BF16),
+                  ("v", v, (B, cfg.h_kv, Tk, cfg.d_v), _BF16), ("out", out, o_shape, _BF16),
+                  ("lse", lse, (B, Tq, Hq), _F32), ("d_out", d_out, o_shape, _BF16))
+    n = _size("nsa_window_bwd_workspace_size", cfg)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws = torch.empty(n, dtype=_U8, device=dev)
+    _run("nsa_window_attn_bwd", dev, cfg, q, k, v, out, lse, d_out, dq, dk, dv, ws, n)
     return dq, dk, dv
 
 
@@ -471,12 +493,13 @@ def paged_attention(cfg: NsaPagedConfig, q, k_pages, v_pages, table, lens):
     """Attention of the newest cfg.seqlen_q tokens over the paged cache on the current stream:
     (out bf16, lse fp32)."""
     B, Tq, Hq = cfg.batch, cfg.seqlen_q, cfg.h_q
-    with _on(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), *_cache(cfg, k_pages, v_pages),
-             *_books(cfg, table, lens)):
-        out = torch.empty(B, Tq, Hq, cfg.d_v, dtype=_BF16, device=q.device)
-        lse = torch.empty(B, Tq, Hq, dtype=_F32, device=q.device)
-        ws = torch.empty(nsa_paged_workspace_size(cfg), dtype=torch.uint8, device=q.device)
-        nsa_paged_attn_fwd(cfg, q, k_pages, v_pages, table, lens, out, lse, ws, ws.numel())
+    dev = _device(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), *_cache(cfg, k_pages, v_pages),
+                  *_books(cfg, table, lens))
+    n = _size("nsa_paged_workspace_size", cfg)
+    out = torch.empty((B, Tq, Hq, cfg.d_v), dtype=_BF16, device=dev)
+    lse = torch.empty((B, Tq, Hq), dtype=_F32, device=dev)
+    ws = torch.empty(n, dtype=_U8, device=dev)
+    _run("nsa_paged_attn_fwd", dev, cfg, q, k_pages, v_pages, table, lens, out, lse, ws, n)
     return out, lse
 
 
@@ -485,22 +508,21 @@ def paged_append(cfg: NsaPagedConfig, k_new, v_new, k_pages, v_pages, table, len
     short_pages [1] int32 on the device: 0, or what was missing (then nothing has changed)."""
     new = (cfg.batch, cfg.h_kv, cfg.seqlen_q)
     extra = () if n_new is None else (("n_new", n_new, (cfg.batch,), _I32),)
-    with _on(("k_new", k_new, new + (cfg.d_qk,), _BF16), ("v_new", v_new, new + (cfg.d_v,), _BF16),
-             *_cache(cfg, k_pages, v_pages), *_books(cfg, table, lens, ref), *extra):
-        short = torch.empty(1, dtype=_I32, device=k_new.device)
-        ws = torch.empty(nsa_paged_append_workspace_size(cfg), dtype=torch.uint8,
-                         device=k_new.device)
-        nsa_paged_append(cfg, k_new, v_new, n_new, k_pages, v_pages, table, lens, ref, short, ws,
-                         ws.numel())
+    dev = _device(("k_new", k_new, new + (cfg.d_qk,), _BF16), ("v_new", v_new, new + (cfg.d_v,), _BF16),
+                  *_cache(cfg, k_pages, v_pages), *_books(cfg, table, lens, ref), *extra)
+    n = _size("nsa_paged_append_workspace_size", cfg)
+    short = torch.empty(1, dtype=_I32, device=dev)
+    ws = torch.empty(n, dtype=_U8, device=dev)
+    _run("nsa_paged_append", dev, cfg, k_new, v_new, n_new, k_pages, v_pages, table, lens, ref, short, ws, n)
     return short
 
 
 def pages_fork(cfg: NsaPagedConfig, src, dst, table, lens, ref):
     """Rows dst share the pages of rows src; returns done [n] int32 (1: carried out)."""
     n = src.numel()
-    with _on(("src", src, (n,), _I32), ("dst", dst, (n,), _I32), *_books(cfg, table, lens, ref)):
-        done = torch.empty(n, dtype=_I32, device=src.device)
-        nsa_pages_fork(cfg, n, src, dst, table, lens, ref, done)
+    dev = _device(("src", src, (n,), _I32), ("dst", dst, (n,), _I32), *_books(cfg, table, lens, ref))
+    done = torch.empty(n, dtype=_I32, device=dev)
+    _run("nsa_pages_fork", dev, cfg, n, src, dst, table, lens, ref, done)
     return done
 
 
@@ -508,18 +530,18 @@ def pages_free(cfg: NsaPagedConfig, rows, table, lens, ref, keep=None):
     """Rows keep their first keep tokens (None: none); returns done [n] int32."""
     n = rows.numel()
     extra = () if keep is None else (("keep", keep, (n,), _I32),)
-    with _on(("rows", rows, (n,), _I32), *_books(cfg, table, lens, ref), *extra):
-        done = torch.empty(n, dtype=_I32, device=rows.device)
-        nsa_pages_free(cfg, n, rows, keep, table, lens, ref, done)
+    dev = _device(("rows", rows, (n,), _I32), *_books(cfg, table, lens, ref), *extra)
+    done = torch.empty(n, dtype=_I32, device=dev)
+    _run("nsa_pages_free", dev, cfg, n, rows, keep, table, lens, ref, done)
     return done
 
 
 def pages_compact(cfg: NsaPagedConfig, k_pages, v_pages, table, lens, ref):
     """Moves the pages in use to the lowest ids, in place; returns (remap [n_pages], n_live [1])."""
-    with _on(*_cache(cfg, k_pages, v_pages), *_books(cfg, table, lens, ref)):
-        dev = table.device
-        remap = torch.empty(cfg.n_pages, dtype=_I32, device=dev)
-        n_live = torch.empty(1, dtype=_I32, device=dev)
-        ws = torch.empty(nsa_pages_compact_workspace_size(cfg), dtype=torch.uint8, device=dev)
-        nsa_pages_compact(cfg, k_pages, v_pages, table, lens, ref, remap, n_live, ws, ws.numel())
+    dev = _device(*_cache(cfg, k_pages, v_pages), *_books(cfg, table, lens, ref))
+    n = _size("nsa_pages_compact_workspace_size", cfg)
+    remap = torch.empty(cfg.n_pages, dtype=_I32, device=dev)
+    n_live = torch.empty(1, dtype=_I32, device=dev)
+    ws = torch.empty(n, dtype=_U8, device=dev)
+    _run("nsa_pages_compact", dev, cfg, k_pages, v_pages, table, lens, ref, remap, n_live, ws, n)
     return remap, n_live

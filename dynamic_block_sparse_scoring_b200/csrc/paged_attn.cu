@@ -23,6 +23,7 @@
 
 #include <algorithm>
 
+#include "launch.cuh"
 #include "paged.cuh"
 #include "tc.cuh"
 
@@ -469,12 +470,11 @@ constexpr int MAX_WORKERS = MAX_SMS * 8;
 template <int DQK, int DV>
 cudaError_t launch_impl(PagedArgs a, int n_units, int rows, cudaStream_t st) {
     using L = Dim<DQK, DV>;
-    int dev = 0, nsm = 148;
-    cudaError_t e = cudaGetDevice(&dev);
+    int dev, nsm;
+    cudaError_t e = sm_count(&nsm, &dev);
     if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(paged_attn_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    static std::atomic<bool> allowed[MAX_DEVICES];
+    e = allow_smem(reinterpret_cast<const void*>(paged_attn_kernel<DQK, DV>), L::SMEM, dev, allowed);
     if (e != cudaSuccess) return e;
     const int grid = std::min(nsm, MAX_SMS);
     paged_attn_kernel<DQK, DV><<<grid, L::WARPS * 32, L::SMEM, st>>>(a);

@@ -10,6 +10,7 @@
 // decode step.
 #include <algorithm>
 
+#include "launch.cuh"
 #include "paged.cuh"
 
 namespace nsa {
@@ -381,8 +382,11 @@ cudaError_t launch_paged_append(const PagedShape& s, const __nv_bfloat16* k_new,
     a.plan = reinterpret_cast<int4*>(ws);
     a.free_list = reinterpret_cast<int32_t*>(ws + up256((size_t)s.B * sizeof(int4)));
     const int smem = s.B * 8;
-    cudaError_t e = cudaFuncSetAttribute(append_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         APPEND_MAX_B * 8);
+    static std::atomic<bool> allowed[MAX_DEVICES];
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = allow_smem(reinterpret_cast<const void*>(append_plan_kernel), APPEND_MAX_B * 8, dev, allowed);
     if (e != cudaSuccess) return e;
     append_plan_kernel<<<1, PLAN_THREADS, smem, st>>>(a);
     e = cudaGetLastError();

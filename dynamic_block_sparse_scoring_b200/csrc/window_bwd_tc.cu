@@ -35,6 +35,7 @@
 
 #include <algorithm>
 
+#include "launch.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
 #include "window.cuh"
@@ -653,11 +654,10 @@ cudaError_t launch_impl(Args a, const __nv_bfloat16* q, const __nv_bfloat16* k, 
                         cudaStream_t st) {
     const WinShape& s = a.s;
     const int planes = s.B * s.Hkv;
-    int dev = 0, nsm = 148;
-    cudaError_t e = cudaGetDevice(&dev);
+    int dev, nsm;
+    cudaError_t e = sm_count(&nsm, &dev);
     if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+    static std::atomic<bool> dq_allowed[MAX_DEVICES], dkv_allowed[MAX_DEVICES];
     const int tok_q = BM / s.G, tok_s = BN / s.G;
     CUtensorMap q128, do128, k64, v64, k128, v128, q64, do64;
     if (!tmap::heads_map(&q128, q, DQK, s.Hq, s.Tq, s.B, s.G, tok_q) ||
@@ -670,7 +670,7 @@ cudaError_t launch_impl(Args a, const __nv_bfloat16* q, const __nv_bfloat16* k, 
     {
         using L = Smem<DQK, DV, DQ>;
         auto kernel = window_bwd_tc_kernel<DQK, DV, DQ>;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+        e = allow_smem(reinterpret_cast<const void*>(kernel), L::ALLOC, dev, dq_allowed);
         if (e != cudaSuccess) return e;
         a.tok = tok_q;
         a.n_tt = ceil_div(s.Tq, tok_q);
@@ -681,7 +681,7 @@ cudaError_t launch_impl(Args a, const __nv_bfloat16* q, const __nv_bfloat16* k, 
     }
     using L = Smem<DQK, DV, DKV>;
     auto kernel = window_bwd_tc_kernel<DQK, DV, DKV>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    e = allow_smem(reinterpret_cast<const void*>(kernel), L::ALLOC, dev, dkv_allowed);
     if (e != cudaSuccess) return e;
     a.tok = tok_s;
     a.n_work = planes * (a.p.nsk * a.p.sp_s + (a.p.nk - a.p.nsk) * a.p.sp_o);

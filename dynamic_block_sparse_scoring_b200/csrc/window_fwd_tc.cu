@@ -30,6 +30,7 @@
 
 #include <algorithm>
 
+#include "launch.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
 #include "window.cuh"
@@ -450,10 +451,8 @@ cudaError_t launch_impl(const WinShape& s, const __nv_bfloat16* q, const __nv_bf
     a.tok = BM / s.G;
     a.n_tt = (s.Tq + a.tok - 1) / a.tok;
     a.scale_log2 = s.scale * 1.4426950408889634f;
-    int dev = 0, nsm = 148;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    int dev, nsm;
+    cudaError_t e = sm_count(&nsm, &dev);
     if (e != cudaSuccess) return e;
     const long long planes = (long long)s.B * s.Hkv;
     // pairs of query tiles unless that would leave SMs without work
@@ -464,7 +463,8 @@ cudaError_t launch_impl(const WinShape& s, const __nv_bfloat16* q, const __nv_bf
         !tmap::rows_map(&mk, k, DQK, s.Tk, s.B * s.Hkv, BN) || !tmap::rows_map(&mv, v, DV, s.Tk, s.B * s.Hkv, BN))
         return cudaErrorInvalidValue;
     const int smem = Smem<DQK, DV>::ALLOC;
-    e = cudaFuncSetAttribute(window_fwd_tc_kernel<DQK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<bool> allowed[MAX_DEVICES];
+    e = allow_smem(reinterpret_cast<const void*>(window_fwd_tc_kernel<DQK, DV>), smem, dev, allowed);
     if (e != cudaSuccess) return e;
     window_fwd_tc_kernel<DQK, DV><<<std::min(a.n_work, nsm), THREADS, smem, st>>>(mq, mk, mv, a);
     return cudaGetLastError();
