@@ -249,13 +249,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const uint32_t last = i + ((nv - 1 - i) / L::VS) * L::VS;
                 tc::mbar_wait_bounded(&bar.v_full[i], (last / L::VS) & 1, WAIT_NS);
             }
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // ------------------------------------------------ MMA issue
+            // The whole warp walks the schedule, one lane issues: with the operands in
+            // uniform registers an MMA costs a few issue slots beside the softmax warps.
             const uint32_t idesc_qk = tc::idesc_bf16_f32(BM, BN, false, false);
             const uint32_t idesc_pv = tc::idesc_bf16_f32(BM, DV, false, true);
-            const uint32_t q_base = tc::smem_u32(sm + L::Q_OFF), k_base = tc::smem_u32(sm + L::K_OFF),
-                           v_base = tc::smem_u32(sm + L::V_OFF);
-            uint32_t nk = 0, nv = 0;            // key / value tiles of the works before this one
+            const uint64_t q_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::Q_OFF), 16, 1024),
+                           k_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::K_OFF), 16, 1024),
+                           v_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::V_OFF), CHUNK, 1024);
+            auto uwait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
+            uint32_t nk = 0;                    // key tiles of the works before this one
             uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
             bool ok = true;
             for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
@@ -271,53 +275,62 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const bool want = j < k.n && needs(s, k, t, j);
                         if (pend[t] >= 0) {
                             const int pj = pend[t];
-                            const uint32_t iv = nv + pj;
-                            if (!wait(&bar.p_full[t], np[t] & 1) ||
-                                !wait(&bar.v_full[iv % L::VS], (iv / L::VS) & 1)) { ok = false; break; }
+                            const uint32_t iv = nk + pj, vs = iv % L::VS;
+                            if (!uwait(&bar.p_full[t], np[t] & 1) || !uwait(&bar.v_full[vs], (iv / L::VS) & 1)) {
+                                ok = false;
+                                break;
+                            }
                             ++np[t];
                             tc::fence_after_sync();
-                            const uint32_t vst = v_base + (iv % L::VS) * L::VC * CHUNK;
+                            const uint64_t vd = tc::desc_at(v_desc, vs * L::VC * CHUNK);
+                            const bool free_v = t == 1 || k.nt == 1 || !needs(s, k, 1, pj);
+                            if (tc::elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < BN / 16; ++kk)
-                                tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
-                                           tc::sdesc_sw128(vst + kk * 2048, CHUNK, 1024), idesc_pv,
-                                           (first[t] && kk == 0) ? 0u : 1u);
+                                for (int kk = 0; kk < BN / 16; ++kk)
+                                    tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
+                                               tc::desc_at(vd, kk * 2048), idesc_pv,
+                                               kk > 0 ? 1u : (first[t] ? 0u : 1u));
+                                if (free_v) tc::mma_commit(&bar.v_empty[vs]);
+                                if (pj == jl[t]) tc::mma_commit(&bar.o_full[t]);
+                            }
+                            __syncwarp();
                             first[t] = false;
-                            if (t == 1 || k.nt == 1 || !needs(s, k, 1, pj)) tc::mma_commit(&bar.v_empty[iv % L::VS]);
-                            if (pj == jl[t]) tc::mma_commit(&bar.o_full[t]);
                             pend[t] = -1;
                         }
                         if (want) {
-                            const uint32_t ik = nk + j;
-                            if (first[t] && !wait(&bar.q_full[t], nq[t] & 1)) { ok = false; break; }
-                            if (!have_k && !wait(&bar.k_full[ik % L::KS], (ik / L::KS) & 1)) { ok = false; break; }
+                            const uint32_t ik = nk + j, ks = ik % L::KS;
+                            if (first[t] && !uwait(&bar.q_full[t], nq[t] & 1)) { ok = false; break; }
+                            if (!have_k && !uwait(&bar.k_full[ks], (ik / L::KS) & 1)) { ok = false; break; }
                             have_k = true;
                             tc::fence_after_sync();
-                            const uint32_t kst = k_base + (ik % L::KS) * L::QC * CHUNK;
+                            const uint64_t qd = tc::desc_at(q_desc, t * L::QC * CHUNK),
+                                           kd = tc::desc_at(k_desc, ks * L::QC * CHUNK);
+                            if (tc::elect_one()) {
 #pragma unroll
-                            for (int kk = 0; kk < DQK / 16; ++kk) {
-                                const uint32_t off = (kk >> 2) * CHUNK + (kk & 3) * 32;
-                                tc::mma_ss(tmem + t * 128, tc::sdesc_sw128(q_base + t * L::QC * CHUNK + off, 16, 1024),
-                                           tc::sdesc_sw128(kst + off, 16, 1024), idesc_qk, kk > 0);
+                                for (int kk = 0; kk < DQK / 16; ++kk) {
+                                    const uint32_t off = (kk >> 2) * CHUNK + (kk & 3) * 32;
+                                    tc::mma_ss(tmem + t * 128, tc::desc_at(qd, off), tc::desc_at(kd, off), idesc_qk,
+                                               kk > 0);
+                                }
+                                tc::mma_commit(&bar.s_full[t]);
+                                if (j == jl[t]) tc::mma_commit(&bar.q_empty[t]);
                             }
-                            tc::mma_commit(&bar.s_full[t]);
-                            if (j == jl[t]) {
-                                tc::mma_commit(&bar.q_empty[t]);
-                                ++nq[t];
-                            }
+                            __syncwarp();
+                            if (j == jl[t]) ++nq[t];
                             pend[t] = j;
                         }
                     }
                     if (ok && j < k.n) {        // (every key tile has a query tile that needs it)
-                        if (!have_k && !wait(&bar.k_full[(nk + j) % L::KS], ((nk + j) / L::KS) & 1)) ok = false;
-                        if (ok) tc::mma_commit(&bar.k_empty[(nk + j) % L::KS]);
+                        const uint32_t ik = nk + j, ks = ik % L::KS;
+                        if (!have_k && !uwait(&bar.k_full[ks], (ik / L::KS) & 1)) ok = false;
+                        if (ok && tc::elect_one()) tc::mma_commit(&bar.k_empty[ks]);
+                        __syncwarp();
                     }
                 }
                 nk += k.n;
-                nv += k.n;
             }
-            if (!ok) give_up();
-            tc::mma_commit(&bar.drain);         // every MMA has completed before TMEM is freed
+            if (!ok && lane == 0) give_up();
+            if (tc::elect_one()) tc::mma_commit(&bar.drain);    // every MMA has completed before TMEM is freed
             tc::mbar_wait_bounded(&bar.drain, 0, WAIT_NS);
         }
         __syncwarp();
