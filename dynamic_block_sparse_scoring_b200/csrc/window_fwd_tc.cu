@@ -29,6 +29,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.cuh"
 #include "tc.cuh"
@@ -78,16 +79,25 @@ struct Args {
 };
 
 // One work item: query tiles tt0 .. tt0 + nt - 1 of one (sequence, KV head) and
-// the key tiles that any of them needs.
+// the key tiles that any of them needs.  Query tile t needs the key tiles
+// [0, c[t]) (sinks) and [f[t], e[t]) (window); e[t] = 0 if it does not exist.
 struct Work {
     int b, kvh, tt0, nt;
-    int pf[2], pl[2];   // first and last position of each query tile
-    int nst;            // key tiles of the sinks
-    int sl;             // sinks before the window: keys [0, sl)
+    int pf[2];          // first position of each query tile
+    int c[2], f[2], e[2];
+    int nst;            // key tiles of the sinks before the window
+    int sl;             // those sinks: keys [0, sl)
     int lo;             // first key of the window's tiles
     int n;              // key tiles in all
+    int last;           // last key that is needed
 
     __device__ __forceinline__ int key(int j) const { return j < nst ? j * BN : lo + (j - nst) * BN; }
+    // keys of tile j, rounded up to 32
+    __device__ __forceinline__ int width(int j) const {
+        const int left = (j < nst ? sl : last + 1) - key(j);
+        return left >= BN ? BN : (left + 31) & ~31;
+    }
+    __device__ __forceinline__ bool needs(int t, int j) const { return j < e[t] && (j >= f[t] || j < c[t]); }
 };
 
 __device__ __forceinline__ Work decode_work(const Args& a, int w) {
@@ -100,33 +110,25 @@ __device__ __forceinline__ Work decode_work(const Args& a, int w) {
     k.b = r / s.Hkv;
     k.kvh = r % s.Hkv;
     k.nt = min(a.nt, a.n_tt - k.tt0);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        k.pf[t] = s.q0 + (k.tt0 + t) * a.tok;
-        k.pl[t] = min(k.pf[t] + a.tok, s.q0 + s.Tq) - 1;
-    }
-    const int last = k.nt == 2 ? k.pl[1] : k.pl[0];
+    k.pf[0] = s.q0 + k.tt0 * a.tok;
+    k.pf[1] = k.pf[0] + a.tok;
+    const int end = s.q0 + s.Tq;
+    k.last = min(k.pf[0] + k.nt * a.tok, end) - 1;
     k.lo = max(0, k.pf[0] - s.win + 1);
     k.sl = min(s.ns, k.lo);
     k.nst = (k.sl + BN - 1) / BN;
     if (k.lo < k.nst * BN) k.lo = k.sl = k.nst = 0;     // they meet: one range from 0
-    k.n = k.nst + (last - k.lo) / BN + 1;
+    k.n = k.nst + (k.last - k.lo) / BN + 1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = max(0, k.pf[t] - s.win + 1), pl = min(k.pf[t] + a.tok, end) - 1;
+        // tiles that start below ns hold sinks (k.nst of them, or some of the one range)
+        k.c[t] = k.nst > 0 ? k.nst : (max(0, s.ns - k.lo) + BN - 1) / BN;
+        k.f[t] = k.nst + (first - k.lo) / BN;
+        k.e[t] = t < k.nt ? k.nst + (pl - k.lo) / BN + 1 : 0;
+        k.c[t] = min(k.c[t], k.e[t]);
+    }
     return k;
-}
-
-// Some row of query tile t sees some key of key tile j.  (The selects keep the
-// work item in registers.)
-__device__ __forceinline__ bool needs(const WinShape& s, const Work& w, int t, int j) {
-    if (t >= w.nt) return false;
-    if (j < w.nst) return true;
-    const int u0 = w.key(j), pf = t ? w.pf[1] : w.pf[0], pl = t ? w.pl[1] : w.pl[0];
-    return u0 <= pl && (u0 + BN - 1 > pf - s.win || u0 < s.ns);
-}
-
-__device__ __forceinline__ int last_needed(const WinShape& s, const Work& w, int t) {
-    int j = w.n - 1;
-    while (j > 0 && !needs(s, w, t, j)) --j;
-    return j;
 }
 
 // Bits k of [0, 32 w + 32) in [lo, hi] for word w.
@@ -182,8 +184,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     };
 
     if (warp < 4) {
-        // 4 x 32 x 88 + 8 x 32 x 208 = 64512, the 384 x 168 registers of the launch
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;" ::: "memory");
+        // 4 x 32 x 104 + 8 x 32 x 200 = 64512, the 384 x 168 registers of the launch
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;" ::: "memory");
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------ Q and K
             uint32_t nq[2] = {0, 0}, nk = 0;
@@ -253,81 +255,82 @@ __global__ void __launch_bounds__(THREADS, 1)
             // ------------------------------------------------ MMA issue
             // The whole warp walks the schedule, one lane issues: with the operands in
             // uniform registers an MMA costs a few issue slots beside the softmax warps.
-            const uint32_t idesc_qk = tc::idesc_bf16_f32(BM, BN, false, false);
             const uint32_t idesc_pv = tc::idesc_bf16_f32(BM, DV, false, true);
             const uint64_t q_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::Q_OFF), 16, 1024),
                            k_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::K_OFF), 16, 1024),
                            v_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::V_OFF), CHUNK, 1024);
             auto uwait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
-            uint32_t nk = 0;                    // key tiles of the works before this one
-            uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
+            uint32_t ks = 0, kph = 0, vs0 = 0, vph0 = 0;    // stage and phase of key tile 0 / value tile 0
+            uint32_t nq = 0, np[2] = {0, 0};                // (nq: works, with bit t kept per tile)
             bool ok = true;
             for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
                 const Work k = decode_work(a, w);
                 int pend[2] = {-1, -1};         // key tile whose P V is still to be issued
                 bool first[2] = {true, true};
-                const int jl[2] = {last_needed(s, k, 0), last_needed(s, k, 1)};
+                uint32_t vs = vs0, vph = vph0;  // of value tile j - 1
+                int wp = 0;                     // width of key tile j - 1
                 for (int j = 0; ok && j <= k.n; ++j) {
-                    bool have_k = false;
+                    const int wj = j < k.n ? k.width(j) : 0;
+                    const uint32_t idesc_w = tc::idesc_bf16_f32(BM, 0, false, false) | ((uint32_t)(wj >> 3) << 17);
+                    const uint64_t kd = tc::desc_at(k_desc, ks * L::QC * CHUNK), vd = tc::desc_at(v_desc, vs * L::VC * CHUNK);
+                    const bool second = j > 0 && k.needs(1, j - 1);
+                    bool have_k = false, have_v = false;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        if (t >= k.nt) continue;
-                        const bool want = j < k.n && needs(s, k, t, j);
-                        if (pend[t] >= 0) {
-                            const int pj = pend[t];
-                            const uint32_t iv = nk + pj, vs = iv % L::VS;
-                            if (!uwait(&bar.p_full[t], np[t] & 1) || !uwait(&bar.v_full[vs], (iv / L::VS) & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            ++np[t];
+                        const bool want = k.needs(t, j), pv = pend[t] >= 0;
+                        const bool last_q = j == k.e[t] - 1, last_p = j == k.e[t];
+                        const uint32_t acc = first[t] ? 0u : 1u;
+                        if (pv) {
+                            if (!have_v && !uwait(&bar.v_full[vs], vph)) { ok = false; break; }
+                            have_v = true;
+                            if (!uwait(&bar.p_full[t], np[t] & 1)) { ok = false; break; }
                             tc::fence_after_sync();
-                            const uint64_t vd = tc::desc_at(v_desc, vs * L::VC * CHUNK);
-                            const bool free_v = t == 1 || k.nt == 1 || !needs(s, k, 1, pj);
                             if (tc::elect_one()) {
 #pragma unroll
                                 for (int kk = 0; kk < BN / 16; ++kk)
-                                    tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
-                                               tc::desc_at(vd, kk * 2048), idesc_pv,
-                                               kk > 0 ? 1u : (first[t] ? 0u : 1u));
-                                if (free_v) tc::mma_commit(&bar.v_empty[vs]);
-                                if (pj == jl[t]) tc::mma_commit(&bar.o_full[t]);
+                                    if (kk * 16 < wp)
+                                        tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
+                                                   tc::desc_at(vd, kk * 2048), idesc_pv, kk > 0 ? 1u : acc);
+                                if (t == 1 || !second) tc::mma_commit(&bar.v_empty[vs]);
+                                if (last_p) tc::mma_commit(&bar.o_full[t]);
                             }
                             __syncwarp();
+                            ++np[t];
                             first[t] = false;
                             pend[t] = -1;
                         }
                         if (want) {
-                            const uint32_t ik = nk + j, ks = ik % L::KS;
-                            if (first[t] && !uwait(&bar.q_full[t], nq[t] & 1)) { ok = false; break; }
-                            if (!have_k && !uwait(&bar.k_full[ks], (ik / L::KS) & 1)) { ok = false; break; }
+                            if (first[t] && !uwait(&bar.q_full[t], (nq >> t) & 1)) { ok = false; break; }
+                            if (!have_k && !uwait(&bar.k_full[ks], kph)) { ok = false; break; }
                             have_k = true;
                             tc::fence_after_sync();
-                            const uint64_t qd = tc::desc_at(q_desc, t * L::QC * CHUNK),
-                                           kd = tc::desc_at(k_desc, ks * L::QC * CHUNK);
+                            const uint64_t qd = tc::desc_at(q_desc, t * L::QC * CHUNK);
                             if (tc::elect_one()) {
 #pragma unroll
                                 for (int kk = 0; kk < DQK / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * CHUNK + (kk & 3) * 32;
-                                    tc::mma_ss(tmem + t * 128, tc::desc_at(qd, off), tc::desc_at(kd, off), idesc_qk,
+                                    tc::mma_ss(tmem + t * 128, tc::desc_at(qd, off), tc::desc_at(kd, off), idesc_w,
                                                kk > 0);
                                 }
                                 tc::mma_commit(&bar.s_full[t]);
-                                if (j == jl[t]) tc::mma_commit(&bar.q_empty[t]);
+                                if (last_q) tc::mma_commit(&bar.q_empty[t]);
                             }
                             __syncwarp();
-                            if (j == jl[t]) ++nq[t];
+                            if (last_q) nq ^= 1u << t;
                             pend[t] = j;
                         }
                     }
                     if (ok && j < k.n) {        // (every key tile has a query tile that needs it)
-                        const uint32_t ik = nk + j, ks = ik % L::KS;
-                        if (!have_k && !uwait(&bar.k_full[ks], (ik / L::KS) & 1)) ok = false;
+                        if (!have_k && !uwait(&bar.k_full[ks], kph)) ok = false;
                         if (ok && tc::elect_one()) tc::mma_commit(&bar.k_empty[ks]);
                         __syncwarp();
+                        if (++ks == L::KS) ks = 0, kph ^= 1;
                     }
+                    if (j > 0 && ++vs == L::VS) vs = 0, vph ^= 1;
+                    wp = wj;
                 }
-                nk += k.n;
+                vs0 = vs;
+                vph0 = vph;
             }
             if (!ok && lane == 0) give_up();
             if (tc::elect_one()) tc::mma_commit(&bar.drain);    // every MMA has completed before TMEM is freed
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;" ::: "memory");
         // ---------------------------------------------------- softmax and epilogue of one query tile
         const int t = (warp - 4) >> 2;
         const int r = (warp & 3) * 32 + lane;                   // row of the tile
@@ -345,18 +348,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ns = 0, no = 0;
         bool ok = true;
         auto warp_wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
+        const uint64_t sc2 = tc::f2_pack(a.scale_log2, a.scale_log2);
         for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
             const Work k = decode_work(a, w);
             if (t >= k.nt) continue;
-            const int pos = (t == 0 ? k.pf[0] : k.pf[1]) + tt;
+            const int pos = (t ? k.pf[1] : k.pf[0]) + tt;
             const bool row_ok = tt < a.tok && pos < s.q0 + s.Tq;
+            const int kc = t ? k.c[1] : k.c[0], kf = t ? k.f[1] : k.f[0], ke = t ? k.e[1] : k.e[0];
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < k.n; ++j) {
-                if (!needs(s, k, t, j)) continue;
-                if (!warp_wait(&bar.s_full[t], ns & 1)) { ok = false; break; }
-                ++ns;
-                tc::fence_after_sync();
-                const int u0 = k.key(j);
+            for (int j = kc > 0 ? 0 : kf, first = 1; j < ke; first = 0, j = j + 1 < kc ? j + 1 : max(j + 1, kf)) {
+                const int u0 = k.key(j), nc = k.width(j) >> 5;
                 // visible offsets: [lo, hi] and, behind the window, [0, sk)
                 int lo, hi, sk;
                 if (j < k.nst) {
@@ -368,54 +369,83 @@ __global__ void __launch_bounds__(THREADS, 1)
                     hi = pos - u0;
                     sk = min(s.ns - u0, hi + 1);
                 }
+                const bool full = __all_sync(0xffffffffu, (hi >= BN - 1 && (lo <= 0 || sk >= BN)) || !row_ok);
+                if (!warp_wait(&bar.s_full[t], ns & 1)) { ok = false; break; }
+                ++ns;
+                tc::fence_after_sync();
+                // all scores of the row in registers; the maximum of the first half is taken
+                // while the second half is on its way
                 uint32_t x[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS + 32 * c, x + 32 * c);
-                tc::tmem_wait_ld();
-                const bool full = hi >= BN - 1 && (lo <= 0 || sk >= BN);
-                if (!__all_sync(0xffffffffu, full || !row_ok)) {
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto load = [&](auto masked_tag) {
+                    constexpr bool MASKED = decltype(masked_tag)::value;
+                    tc::tmem_ld32(tS, x);
+                    if (!MASKED || nc > 1) tc::tmem_ld32(tS + 32, x + 32);
+                    tc::tmem_wait_ld32(x);
+                    tc::tmem_wait_ld32(x + 32);
+                    if (!MASKED || nc > 2) tc::tmem_ld32(tS + 64, x + 64);
+                    if (!MASKED || nc > 3) tc::tmem_ld32(tS + 96, x + 96);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const uint32_t bits = range_bits(lo, hi, c) | range_bits(0, sk - 1, c);
+                        if (MASKED && c >= nc) break;
+                        if (c == 2) {
+                            tc::tmem_wait_ld32(x + 64);
+                            tc::tmem_wait_ld32(x + 96);
+                        }
+                        if (MASKED) {
+                            const uint32_t bits = range_bits(lo, hi, c) | range_bits(0, sk - 1, c);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((bits >> i) & 1u)) x[32 * c + i] = 0xFF800000u;
+                            for (int i = 0; i < 32; ++i)
+                                if (!((bits >> i) & 1u)) x[32 * c + i] = 0xFF800000u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2)
+                            mx[(i >> 1) & 3] = tc::max3(mx[(i >> 1) & 3], __uint_as_float(x[32 * c + i]),
+                                                        __uint_as_float(x[32 * c + i + 1]));
                     }
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+                };
+                if (full) load(std::false_type{});
+                else load(std::true_type{});
                 // scale > 0, so the scaled maximum is the maximum of the scaled scores
                 const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-                float alpha = 1.f;
+                float alpha = 1.f;                              // for what was summed under the reference before
                 if (mt > m + 8.f || m == -INFINITY) {           // (-inf > -inf is false: m stays)
                     if (m != -INFINITY) alpha = tc::ex2(m - mt);
                     m = mt;
                 }
                 const float neg = m == -INFINITY ? 0.f : -m;
-                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t neg2 = tc::f2_pack(neg, neg);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int i = 0; i < 128; i += 2) {
-                    const float p0 = tc::ex2(fmaf(__uint_as_float(x[i]), a.scale_log2, neg));
-                    const float p1 = tc::ex2(fmaf(__uint_as_float(x[i + 1]), a.scale_log2, neg));
-                    ps[(i >> 1) & 3] += p0 + p1;
-                    x[i >> 1] = tc::pack_bf16x2(p0, p1);        // packed in place: i / 2 <= i
+                for (int c = 0; c < 4; ++c) {
+                    if (c >= nc) break;         // (also keeps the chunks' code apart: fewer values live at once)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float y0, y1;
+                        tc::f2_unpack(tc::f2_fma(tc::f2_pack(__uint_as_float(x[32 * c + i]),
+                                                             __uint_as_float(x[32 * c + i + 1])), sc2, neg2), y0, y1);
+                        const float p0 = tc::ex2(y0), p1 = tc::ex2(y1);
+                        sum[(i >> 1) & 1] = tc::f2_add(sum[(i >> 1) & 1], tc::f2_pack(p0, p1));
+                        x[16 * c + (i >> 1)] = tc::pack_bf16x2(p0, p1);     // in place: 16 c + i / 2 <= 32 c + i
+                    }
+                    tc::tmem_st16(tS + 16 * c, x + 16 * c);
                 }
-                tc::tmem_st32(tS, x);
-                tc::tmem_st32(tS + 32, x + 32);
+                float s0, s1;
+                tc::f2_unpack(tc::f2_add(sum[0], sum[1]), s0, s1);
+                const float psum = s0 + s1;
                 if (__any_sync(0xffffffffu, alpha != 1.f)) {    // O holds the tiles before this one
 #pragma unroll 1
                     for (int c = 0; c < DV; c += 32) {
                         uint32_t o[32];
                         tc::tmem_ld32(tO + c, o);
-                        tc::tmem_wait_ld();
+                        tc::tmem_wait_ld32(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
                         tc::tmem_st32(tO + c, o);
                     }
                     l *= alpha;
                 }
-                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                l += psum;
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -431,7 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int c = 0; c < DV; c += 32) {
                 uint32_t o[32];
                 tc::tmem_ld32(tO + c, o);
-                tc::tmem_wait_ld();
+                tc::tmem_wait_ld32(o);
                 if (row_ok) {
                     uint4* dst = reinterpret_cast<uint4*>(a.out + row * DV + c);
 #pragma unroll
@@ -442,6 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         dst[q] = pack8(f);
                     }
                 }
+                __syncwarp();
             }
             if (row_ok && a.lse) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
             tc::fence_before_sync();
