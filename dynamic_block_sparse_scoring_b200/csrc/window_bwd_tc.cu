@@ -280,66 +280,85 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::mbar_wait_bounded(&bar.t_full[i], (last / L::NST) & 1, WAIT_NS);
             }
             if (nr > 0) tc::mbar_wait_bounded(&bar.r_full, (nr - 1) & 1, WAIT_NS);
-        } else if (warp == 1 && lane == 0) {
+        } else if (warp == 1) {
             // ------------------------------------------------ MMA issue
+            // The whole warp walks the schedule, one lane issues: the operands stay in
+            // uniform registers.
             const uint32_t idesc_sd = tc::idesc_bf16_f32(BM, BN, false, false);
             const uint32_t idesc_q = tc::idesc_bf16_f32(BM, DQK, false, true);
             const uint32_t idesc_v = tc::idesc_bf16_f32(BM, DV, false, true);
-            const uint32_t r_base = tc::smem_u32(sm), t_base = tc::smem_u32(sm + L::T_OFF);
-            uint32_t g = 0, works = 0;          // steps and works before this work
+            const uint64_t r_desc = tc::sdesc_sw128(tc::smem_u32(sm), 16, 1024),
+                           t_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::T_OFF), 16, 1024),      // K-major
+                           g_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::T_OFF), TCHUNK, 1024);  // MN-major
+            const uint32_t tG = tmem + L::ACC_COL, tGq = MODE == DKV ? tG + DV : tG;
+            uint32_t g = 0, works = 0;          // steps whose scores are issued, works before this one
+            uint32_t sst = 0, sph = 0, gst = 0; // stage (and phase) of the next scores, of the next gradients
             bool ok = true;
-            auto scores = [&](uint32_t e) {     // S and D of step e
-                const int st = e % L::NST, b = e & 1;
-                if (!wait(&bar.t_full[st], (e / L::NST) & 1)) return false;
+            auto scores = [&]() {               // S and D of step g
+                const uint32_t e = g, b = e & 1;
+                const uint64_t td = tc::desc_at(t_desc, sst * L::T_BYTES);
+                if (!warp_wait(&bar.t_full[sst], sph)) return false;
                 tc::fence_after_sync();
-                const uint32_t t0 = t_base + st * L::T_BYTES;
+                if (tc::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < DQK / 16; ++kk)
-                    tc::mma_ss(tmem + b * 64, tc::sdesc_sw128(r_base + (kk >> 2) * RCHUNK + (kk & 3) * 32, 16, 1024),
-                               tc::sdesc_sw128(t0 + (kk >> 2) * TCHUNK + (kk & 3) * 32, 16, 1024), idesc_sd, kk > 0);
-                tc::mma_commit(&bar.s_full[b]);
+                    for (int kk = 0; kk < DQK / 16; ++kk)
+                        tc::mma_ss(tmem + b * 64, tc::desc_at(r_desc, (kk >> 2) * RCHUNK + (kk & 3) * 32),
+                                   tc::desc_at(td, (kk >> 2) * TCHUNK + (kk & 3) * 32), idesc_sd, kk > 0);
+                    tc::mma_commit(&bar.s_full[b]);
+                }
+                __syncwarp();
                 // one D buffer: the step before this one must have read it
-                if (L::ND == 1 && e > 0 && !wait(&bar.d_read[b ^ 1], ((e - 1) >> 1) & 1)) return false;
+                if (L::ND == 1 && e > 0 && !warp_wait(&bar.d_read[b ^ 1], ((e - 1) >> 1) & 1)) return false;
                 tc::fence_after_sync();
                 const uint32_t tD = tmem + L::D_COL + (L::ND == 2 ? b * 64 : 0);
+                if (tc::elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < DV / 16; ++kk)
-                    tc::mma_ss(tD, tc::sdesc_sw128(r_base + (L::QC + (kk >> 2)) * RCHUNK + (kk & 3) * 32, 16, 1024),
-                               tc::sdesc_sw128(t0 + (L::QC + (kk >> 2)) * TCHUNK + (kk & 3) * 32, 16, 1024), idesc_sd,
-                               kk > 0);
-                tc::mma_commit(&bar.d_full[b]);
+                    for (int kk = 0; kk < DV / 16; ++kk)
+                        tc::mma_ss(tD, tc::desc_at(r_desc, (L::QC + (kk >> 2)) * RCHUNK + (kk & 3) * 32),
+                                   tc::desc_at(td, (L::QC + (kk >> 2)) * TCHUNK + (kk & 3) * 32), idesc_sd, kk > 0);
+                    tc::mma_commit(&bar.d_full[b]);
+                }
+                __syncwarp();
+                if (++sst == L::NST) sst = 0, sph ^= 1;
+                ++g;
                 return true;
             };
             for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
                 Work k;
                 if (!decode_work<MODE>(a, w, &k) || k.n == 0) continue;
-                if (!wait(&bar.r_full, works & 1) || !scores(g)) { ok = false; break; }
-                for (int i = 0; i < k.n; ++i, ++g) {
-                    if (i + 1 < k.n && !scores(g + 1)) { ok = false; break; }
-                    if (i + 1 == k.n) tc::mma_commit(&bar.r_empty);     // the residents' last use
-                    const int st = g % L::NST, b = g & 1;
-                    if (!wait(&bar.p_full[b], (g >> 1) & 1)) { ok = false; break; }
-                    if (i == 0 && !wait(&bar.acc_free, (works & 1) ^ 1)) { ok = false; break; }
+                if (!warp_wait(&bar.r_full, works & 1) || !scores()) { ok = false; break; }
+                for (int i = 0; i < k.n; ++i) {
+                    const uint32_t e = g - 1, b = e & 1;        // the step of these gradients
+                    if (i + 1 < k.n && !scores()) { ok = false; break; }
+                    if (i + 2 == k.n || k.n == 1) {             // the residents' last use is issued
+                        if (tc::elect_one()) tc::mma_commit(&bar.r_empty);
+                        __syncwarp();
+                    }
+                    const uint64_t gd = tc::desc_at(g_desc, gst * L::T_BYTES);
+                    const uint32_t tA = tmem + b * 64, tAq = MODE == DKV ? tA + 32 : tA, acc = i > 0 ? 1u : 0u;
+                    if (i == 0 && !warp_wait(&bar.acc_free, (works & 1) ^ 1)) { ok = false; break; }
+                    if (!warp_wait(&bar.p_full[b], (e >> 1) & 1)) { ok = false; break; }
                     tc::fence_after_sync();
-                    const uint32_t t0 = t_base + st * L::T_BYTES, tA = tmem + b * 64, tG = tmem + L::ACC_COL;
-                    if (MODE == DKV) {
+                    if (tc::elect_one()) {
+                        if (MODE == DKV) {
+#pragma unroll
+                            for (int kk = 0; kk < BN / 16; ++kk)
+                                tc::mma_ts(tG, tA + kk * 8, tc::desc_at(gd, L::QC * TCHUNK + kk * 2048), idesc_v,
+                                           kk > 0 ? 1u : acc);
+                        }
 #pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk)
-                            tc::mma_ts(tG, tA + kk * 8, tc::sdesc_sw128(t0 + L::QC * TCHUNK + kk * 2048, TCHUNK, 1024),
-                                       idesc_v, (i > 0 || kk > 0) ? 1u : 0u);
+                            tc::mma_ts(tGq, tAq + kk * 8, tc::desc_at(gd, kk * 2048), idesc_q, kk > 0 ? 1u : acc);
+                        tc::mma_commit(&bar.t_empty[gst]);
+                        if (i + 1 == k.n) tc::mma_commit(&bar.acc_full);
                     }
-                    const uint32_t tGq = MODE == DKV ? tG + DV : tG, tAq = MODE == DKV ? tA + 32 : tA;
-#pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)
-                        tc::mma_ts(tGq, tAq + kk * 8, tc::sdesc_sw128(t0 + kk * 2048, TCHUNK, 1024), idesc_q,
-                                   (i > 0 || kk > 0) ? 1u : 0u);
-                    tc::mma_commit(&bar.t_empty[st]);
+                    __syncwarp();
+                    if (++gst == L::NST) gst = 0;
                 }
-                if (ok) tc::mma_commit(&bar.acc_full);
                 ++works;
             }
-            if (!ok) give_up();
-            tc::mma_commit(&bar.drain);         // every MMA has completed before TMEM is freed
+            if (!ok && lane == 0) give_up();
+            if (tc::elect_one()) tc::mma_commit(&bar.drain);    // every MMA has completed before TMEM is freed
             tc::mbar_wait_bounded(&bar.drain, 0, WAIT_NS);
         } else if (MODE == DQ && warp >= 2) {
             // ------------------------------------------------ (lse, delta) of a query tile's rows
