@@ -36,6 +36,7 @@
 #include <algorithm>
 
 #include "launch.cuh"
+#include "rows_out.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
 #include "window.cuh"
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t tS = tmem + wg * 64 + lane_off;
         const uint32_t tD = tmem + L::D_COL + (L::ND == 2 ? wg * 64 : 0) + lane_off;
         const uint32_t tG = tmem + L::ACC_COL + lane_off;
-        const int tt = r / s.G, gh = r - tt * s.G;
+        const int tt = r / s.G;
         uint32_t g = 0, works = 0, n = 0;
         bool ok = true;
         for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
@@ -552,47 +553,37 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!warp_wait(&bar.acc_full, works & 1)) { ok = false; break; }
                 tc::fence_after_sync();
             }
-            // this warpgroup's 32-column pieces of the accumulator row
-            size_t qrow = 0;
-            bool row_ok;
-            if (MODE == DQ) {
-                row_ok = tt < a.tok && k.first + tt < s.Tq;
-                qrow = ((size_t)k.b * s.Tq + k.first + tt) * s.Hq + k.kvh * s.G + gh;
-            } else {
-                row_ok = pos < s.Tk;
-                qrow = ((size_t)k.b * s.Hkv + k.kvh) * s.Tk + pos;
+            // this warpgroup's 32-column pieces of the accumulator rows
+            OutRows rows;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int rj = (r & ~3) + j;
+                if (MODE == DQ) {
+                    const int tj = rj / s.G, i = k.first + tj;
+                    rows.off[j] = tj < a.tok && i < s.Tq
+                                      ? ((long long)k.b * s.Tq + i) * s.Hq + k.kvh * s.G + (rj - tj * s.G)
+                                      : -1;
+                } else {
+                    const int u = k.first + rj;
+                    rows.off[j] = u >= s.Tk       ? -1
+                                  : k.slot >= 0 ? (long long)k.slot * BM + rj
+                                                : ((long long)k.b * s.Hkv + k.kvh) * s.Tk + u;
+                }
             }
 #pragma unroll 1
             for (int c = wg * 32; c < L::ACC; c += 64) {
                 uint32_t o[32];
                 if (k.n > 0) {
                     tc::tmem_ld32(tG + c, o);
-                    tc::tmem_wait_ld();
+                    tc::tmem_wait_ld32(o);
                 } else {                            // keys that no query sees
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
-                if (row_ok && MODE == DKV && k.slot >= 0) {
-                    float4* dst = reinterpret_cast<float4*>(a.part + ((size_t)k.slot * BM + r) * L::ACC + c);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        dst[q] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                                             __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
-                } else if (row_ok) {
-                    const bool val = MODE == DKV && c < DV;
-                    const float f = val ? 1.f : s.scale;
-                    __nv_bfloat16* row = MODE == DQ ? a.dq + qrow * DQK + c
-                                         : val      ? a.dv + qrow * DV + c
-                                                    : a.dk + qrow * DQK + (c - DV);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float z[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) z[e] = __uint_as_float(o[8 * q + e]) * f;
-                        reinterpret_cast<uint4*>(row)[q] = pack8(z);
-                    }
-                }
-                __syncwarp();
+                if (MODE == DQ) store_bf16x32(o, s.scale, a.dq, rows, DQK, c, lane);
+                else if (k.slot >= 0) store_f32x32(o, a.part, rows, L::ACC, c, lane);
+                else if (c < DV) store_bf16x32(o, 1.f, a.dv, rows, DV, c, lane);
+                else store_bf16x32(o, s.scale, a.dk, rows, DQK, c - DV, lane);
             }
             if (k.n > 0) {
                 tc::fence_before_sync();

@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "launch.cuh"
+#include "rows_out.cuh"
 #include "tc.cuh"
 #include "tmap.cuh"
 #include "window.cuh"
@@ -455,26 +456,25 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!warp_wait(&bar.o_full[t], no & 1)) { ok = false; break; }
             ++no;
             tc::fence_after_sync();
-            const size_t row = ((size_t)k.b * s.Tq + (pos - s.q0)) * s.Hq + k.kvh * s.G + g;
+            OutRows rows;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int rj = (r & ~3) + j, tj = rj / s.G, i = (k.tt0 + t) * a.tok + tj;
+                rows.off[j] = tj < a.tok && i < s.Tq
+                                  ? ((long long)k.b * s.Tq + i) * s.Hq + k.kvh * s.G + (rj - tj * s.G)
+                                  : -1;
+            }
             const float inv = 1.f / l;
 #pragma unroll 1
             for (int c = 0; c < DV; c += 32) {
                 uint32_t o[32];
                 tc::tmem_ld32(tO + c, o);
                 tc::tmem_wait_ld32(o);
-                if (row_ok) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.out + row * DV + c);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float f[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[8 * q + e]) * inv;
-                        dst[q] = pack8(f);
-                    }
-                }
-                __syncwarp();
+                store_bf16x32(o, inv, a.out, rows, DV, c, lane);
             }
-            if (row_ok && a.lse) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+            if (row_ok && a.lse)
+                a.lse[((size_t)k.b * s.Tq + (pos - s.q0)) * s.Hq + k.kvh * s.G + g] =
+                    (m + log2f(l)) * 0.6931471805599453f;
             tc::fence_before_sync();
         }
         if (!ok) give_up();
