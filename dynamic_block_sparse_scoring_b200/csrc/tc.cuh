@@ -59,6 +59,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* b, uint32_t parity) {
     return ok != 0;
 }
 
+// The same without suspending the thread: has the phase completed?
+__device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Waits until the phase of `b` with parity `parity` has completed.  Gives up
 // after `limit_ns` of wall time, or as soon as another role of the CTA has
 // raised `*abort`, and returns false; the caller then unwinds.
@@ -375,6 +388,14 @@ __device__ __forceinline__ void mma_ss_tf32(uint32_t d_tmem, uint64_t a_desc, ui
 __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The same for K-major rows of 32 bytes (16 bf16), 32-byte swizzle: 8-row groups
+// of 256 B, 256-byte aligned; the 16-byte half of a row is exchanged in rows 4-7
+// of a group (byte = row * 32 + ((half ^ (row >> 2 & 1)) << 4)).
+__device__ __forceinline__ uint64_t sdesc_sw32(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(256 >> 4) << 32) |
+           (1ull << 46) | (6ull << 61);
 }
 
 // D[tmem] (+)= A[smem] * B[smem]

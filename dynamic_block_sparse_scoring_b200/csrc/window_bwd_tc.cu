@@ -63,9 +63,13 @@ struct Smem {
     static constexpr int R_BYTES = (QC + VC) * RCHUNK, T_BYTES = (QC + VC) * TCHUNK;
     static constexpr int NST = (216 * 1024 - R_BYTES) / T_BYTES >= 4 ? 4 : 3;
     static constexpr int T_OFF = R_BYTES;
-    static constexpr int AUX_OFF = T_OFF + NST * T_BYTES;       // float2 (lse log2 e, delta)
-    static constexpr int AUX = MODE == DQ ? 2 * BM : NST * BN;  // two query tiles / one per stage
-    static constexpr int BAR_OFF = AUX_OFF + AUX * 8;
+    // DQ: float2 (lse log2 e, delta) of the rows of two query tiles.  DKV: 16 more columns for
+    // the products, 32 bytes a row: a constant [BM] of the residents, then per stage [BN] for S, [BN] for D
+    static constexpr int AUX_OFF = T_OFF + NST * T_BYTES;
+    static constexpr int EXT_A = BM * 32, EXT_B = BN * 32;
+    static constexpr int AUX_BYTES = MODE == DQ ? 2 * BM * 8 : EXT_A + NST * 2 * EXT_B;
+    static constexpr int BAR_OFF = AUX_OFF + AUX_BYTES;
+    static_assert(AUX_OFF % 1024 == 0, "swizzled rows");
     static constexpr int ALLOC = BAR_OFF + 512 + 1024;
     static constexpr int ACC = MODE == DQ ? DQK : DQK + DV;     // accumulator columns
     static constexpr int ND = 128 + 128 + ACC <= 512 ? 2 : 1;   // D buffers in TMEM
@@ -74,7 +78,7 @@ struct Smem {
 
 struct Bars {
     uint64_t r_full, r_empty, t_full[4], t_empty[4], s_full[2], d_full[2], d_read[2], p_full[2];
-    uint64_t acc_full, acc_free, aux_full[4], aux_empty[2], drain;
+    uint64_t acc_full, acc_free, aux_full[2], aux_empty[2], drain;
     uint32_t tmem;
     int abort;
 };
@@ -191,15 +195,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::mbar_init(&bar.r_full, 1);
         tc::mbar_init(&bar.r_empty, 1);
         for (int i = 0; i < 4; ++i) {
-            tc::mbar_init(&bar.t_full[i], 1);
+            tc::mbar_init(&bar.t_full[i], MODE == DKV ? 2 : 1);     // the copies, and the (lse, delta) columns
             tc::mbar_init(&bar.t_empty[i], 1);
-            tc::mbar_init(&bar.aux_full[i], MODE == DQ ? 2 : 1);
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bar.s_full[i], 1);
             tc::mbar_init(&bar.d_full[i], 1);
             tc::mbar_init(&bar.d_read[i], 4);
             tc::mbar_init(&bar.p_full[i], 4);
+            tc::mbar_init(&bar.aux_full[i], 2);
             tc::mbar_init(&bar.aux_empty[i], 8);
         }
         tc::mbar_init(&bar.acc_full, 1);
@@ -216,6 +220,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         // rows of a step that no query fills stay zero: they enter the sums over rows
         for (int i = threadIdx.x; i < L::NST * L::T_BYTES / 16; i += THREADS)
             reinterpret_cast<uint4*>(sm + L::T_OFF)[i] = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+    }
+    if (MODE == DKV && threadIdx.x < BM) {          // (1, 1, 1, 0, ..) in every row of the constant
+        const int half = (threadIdx.x >> 2) & 1;
+        uint4* row = reinterpret_cast<uint4*>(sm + L::AUX_OFF + threadIdx.x * 32);
+        row[half] = make_uint4(0x3F803F80u, 0x00003F80u, 0, 0);
+        row[half ^ 1] = make_uint4(0, 0, 0, 0);
         tc::fence_proxy_async_smem();
     }
     if (warp == 1) {
@@ -291,46 +302,69 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint64_t r_desc = tc::sdesc_sw128(tc::smem_u32(sm), 16, 1024),
                            t_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::T_OFF), 16, 1024),      // K-major
                            g_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::T_OFF), TCHUNK, 1024);  // MN-major
+            const uint64_t x_desc = tc::sdesc_sw32(tc::smem_u32(sm + L::AUX_OFF));
             const uint32_t tG = tmem + L::ACC_COL, tGq = MODE == DKV ? tG + DV : tG;
             uint32_t g = 0, works = 0;          // steps whose scores are issued, works before this one
             uint32_t sst = 0, sph = 0, gst = 0; // stage (and phase) of the next scores, of the next gradients
             bool ok = true;
-            auto scores = [&]() {               // S and D of step g
+            // The tensor pipe queues only a few MMAs, so a gap of 100 clocks between them is a
+            // stall: each barrier is tested (soon) in the middle of the issue before it is
+            // needed, and waited for only if it was not there yet.
+            auto soon = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_test(b, parity)); };
+            bool t_soon = false;
+            // S and D of step g; p_bar: the barrier that is needed next (null: none), *p_soon: it is there
+            auto scores = [&](uint64_t* p_bar, uint32_t p_parity, bool* p_soon) {
                 const uint32_t e = g, b = e & 1;
                 const uint64_t td = tc::desc_at(t_desc, sst * L::T_BYTES);
-                if (!warp_wait(&bar.t_full[sst], sph)) return false;
-                tc::fence_after_sync();
-                if (tc::elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < DQK / 16; ++kk)
-                        tc::mma_ss(tmem + b * 64, tc::desc_at(r_desc, (kk >> 2) * RCHUNK + (kk & 3) * 32),
-                                   tc::desc_at(td, (kk >> 2) * TCHUNK + (kk & 3) * 32), idesc_sd, kk > 0);
-                    tc::mma_commit(&bar.s_full[b]);
-                }
-                __syncwarp();
-                // one D buffer: the step before this one must have read it
-                if (L::ND == 1 && e > 0 && !warp_wait(&bar.d_read[b ^ 1], ((e - 1) >> 1) & 1)) return false;
-                tc::fence_after_sync();
+                const uint64_t xd = tc::desc_at(x_desc, L::EXT_A + sst * 2 * L::EXT_B);
                 const uint32_t tD = tmem + L::D_COL + (L::ND == 2 ? b * 64 : 0);
-                if (tc::elect_one()) {
+                if (!t_soon && !warp_wait(&bar.t_full[sst], sph)) return false;
+                tc::fence_after_sync();
+                bool d_soon = true;
 #pragma unroll
-                    for (int kk = 0; kk < DV / 16; ++kk)
-                        tc::mma_ss(tD, tc::desc_at(r_desc, (L::QC + (kk >> 2)) * RCHUNK + (kk & 3) * 32),
-                                   tc::desc_at(td, (L::QC + (kk >> 2)) * TCHUNK + (kk & 3) * 32), idesc_sd, kk > 0);
-                    tc::mma_commit(&bar.d_full[b]);
+                for (int part = 0; part < 2; ++part) {
+                    if (tc::elect_one()) {
+#pragma unroll
+                        for (int kk = part * (DQK / 32); kk < (part + 1) * (DQK / 32); ++kk)
+                            tc::mma_ss(tmem + b * 64, tc::desc_at(r_desc, (kk >> 2) * RCHUNK + (kk & 3) * 32),
+                                       tc::desc_at(td, (kk >> 2) * TCHUNK + (kk & 3) * 32), idesc_sd, kk > 0);
+                        if (MODE == DKV && part == 1) tc::mma_ss(tmem + b * 64, x_desc, xd, idesc_sd, 1);
+                        if (part == 1) tc::mma_commit(&bar.s_full[b]);
+                    }
+                    __syncwarp();
+                    // one D buffer: the step before this one must have read it
+                    if (L::ND == 1 && part == 0 && e > 0) d_soon = soon(&bar.d_read[b ^ 1], ((e - 1) >> 1) & 1);
                 }
-                __syncwarp();
+                if (L::ND == 1) {
+                    if (!d_soon && !warp_wait(&bar.d_read[b ^ 1], ((e - 1) >> 1) & 1)) return false;
+                    tc::fence_after_sync();
+                }
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    if (tc::elect_one()) {
+#pragma unroll
+                        for (int kk = part * (DV / 32); kk < (part + 1) * (DV / 32); ++kk)
+                            tc::mma_ss(tD, tc::desc_at(r_desc, (L::QC + (kk >> 2)) * RCHUNK + (kk & 3) * 32),
+                                       tc::desc_at(td, (L::QC + (kk >> 2)) * TCHUNK + (kk & 3) * 32), idesc_sd, kk > 0);
+                        if (MODE == DKV && part == 1) tc::mma_ss(tD, x_desc, tc::desc_at(xd, L::EXT_B), idesc_sd, 1);
+                        if (part == 1) tc::mma_commit(&bar.d_full[b]);
+                    }
+                    __syncwarp();
+                    if (part == 0 && p_bar) *p_soon = soon(p_bar, p_parity);
+                }
                 if (++sst == L::NST) sst = 0, sph ^= 1;
+                t_soon = false;
                 ++g;
                 return true;
             };
             for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
                 Work k;
                 if (!decode_work<MODE>(a, w, &k) || k.n == 0) continue;
-                if (!warp_wait(&bar.r_full, works & 1) || !scores()) { ok = false; break; }
+                if (!warp_wait(&bar.r_full, works & 1) || !scores(nullptr, 0, nullptr)) { ok = false; break; }
                 for (int i = 0; i < k.n; ++i) {
                     const uint32_t e = g - 1, b = e & 1;        // the step of these gradients
-                    if (i + 1 < k.n && !scores()) { ok = false; break; }
+                    bool p_soon = false;
+                    if (i + 1 < k.n && !scores(&bar.p_full[b], (e >> 1) & 1, &p_soon)) { ok = false; break; }
                     if (i + 2 == k.n || k.n == 1) {             // the residents' last use is issued
                         if (tc::elect_one()) tc::mma_commit(&bar.r_empty);
                         __syncwarp();
@@ -338,22 +372,31 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint64_t gd = tc::desc_at(g_desc, gst * L::T_BYTES);
                     const uint32_t tA = tmem + b * 64, tAq = MODE == DKV ? tA + 32 : tA, acc = i > 0 ? 1u : 0u;
                     if (i == 0 && !warp_wait(&bar.acc_free, (works & 1) ^ 1)) { ok = false; break; }
-                    if (!warp_wait(&bar.p_full[b], (e >> 1) & 1)) { ok = false; break; }
+                    if (!p_soon && !warp_wait(&bar.p_full[b], (e >> 1) & 1)) { ok = false; break; }
                     tc::fence_after_sync();
-                    if (tc::elect_one()) {
-                        if (MODE == DKV) {
 #pragma unroll
-                            for (int kk = 0; kk < BN / 16; ++kk)
-                                tc::mma_ts(tG, tA + kk * 8, tc::desc_at(gd, L::QC * TCHUNK + kk * 2048), idesc_v,
-                                           kk > 0 ? 1u : acc);
+                    for (int part = 0; part < 2; ++part) {
+                        if (tc::elect_one()) {
+                            if (MODE == DKV && part == 0) {
+#pragma unroll
+                                for (int kk = 0; kk < BN / 16; ++kk)
+                                    tc::mma_ts(tG, tA + kk * 8, tc::desc_at(gd, L::QC * TCHUNK + kk * 2048), idesc_v,
+                                               kk > 0 ? 1u : acc);
+                            }
+                            if (MODE == DQ || part == 1) {
+#pragma unroll
+                                for (int kk = MODE == DQ ? part * 2 : 0; kk < (MODE == DQ ? part * 2 + 2 : 4); ++kk)
+                                    tc::mma_ts(tGq, tAq + kk * 8, tc::desc_at(gd, kk * 2048), idesc_q,
+                                               kk > 0 ? 1u : acc);
+                            }
+                            if (part == 1) {
+                                tc::mma_commit(&bar.t_empty[gst]);
+                                if (i + 1 == k.n) tc::mma_commit(&bar.acc_full);
+                            }
                         }
-#pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)
-                            tc::mma_ts(tGq, tAq + kk * 8, tc::desc_at(gd, kk * 2048), idesc_q, kk > 0 ? 1u : acc);
-                        tc::mma_commit(&bar.t_empty[gst]);
-                        if (i + 1 == k.n) tc::mma_commit(&bar.acc_full);
+                        __syncwarp();
+                        if (part == 0) t_soon = soon(&bar.t_full[sst], sph);    // the next step's rows
                     }
-                    __syncwarp();
                     if (++gst == L::NST) gst = 0;
                 }
                 ++works;
@@ -412,8 +455,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok) give_up();
         } else if (MODE == DKV && warp == 2) {
             // ------------------------------------------------ (lse, delta) of a step's rows
+            // As 16 more columns of the products: -lse / scale and -delta, each the sum of
+            // three bf16 (24 bits), against the residents' (1, 1, 1, 0, ..).  S and D then come
+            // as q.k - lse / scale and do.v - delta, and the threads, whose columns the
+            // queries are, need no other value of theirs.
             uint32_t g = 0;
             bool ok = true;
+            const float inv_scale = 1.f / s.scale;
+            auto three = [](float v) {
+                const __nv_bfloat16 h = __float2bfloat16_rn(v);
+                const float r1 = v - bf2f(h);
+                const __nv_bfloat16 m = __float2bfloat16_rn(r1);
+                return make_uint4(tc::pack_bf16x2(bf2f(h), bf2f(m)), tc::pack_bf16x2(r1 - bf2f(m), 0.f), 0, 0);
+            };
             for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
                 Work k;
                 if (!decode_work<MODE>(a, w, &k) || k.n == 0) continue;
@@ -423,17 +477,25 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = lane + 32 * e, tt = r / s.G, tok = k.base + i * a.tok + tt;
-                        v[e] = make_float2(INFINITY, 0.f);      // p = 0: no query
+                        v[e] = make_float2(-1e30f, 0.f);        // p = 0: no query
                         if (tt < a.tok && tok < s.Tq) {
                             const size_t row = ((size_t)k.b * s.Tq + tok) * s.Hq + k.kvh * s.G + (r - tt * s.G);
-                            v[e] = make_float2(a.lse[row] * LOG2E, a.delta[row]);
+                            v[e] = make_float2(-a.lse[row] * inv_scale, -a.delta[row]);
                         }
                     }
                     if (!warp_wait(&bar.t_empty[st], ((g / L::NST) & 1) ^ 1)) { ok = false; break; }
-                    aux[st * BN + lane] = v[0];
-                    aux[st * BN + lane + 32] = v[1];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = lane + 32 * e, half = (r >> 2) & 1;
+                        uint4* x = reinterpret_cast<uint4*>(sm + L::AUX_OFF + L::EXT_A + st * 2 * L::EXT_B + r * 32);
+                        x[half] = three(v[e].x);
+                        x[half ^ 1] = make_uint4(0, 0, 0, 0);
+                        x[L::EXT_B / 16 + half] = three(v[e].y);
+                        x[L::EXT_B / 16 + (half ^ 1)] = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar.aux_full[st]);
+                    if (lane == 0) tc::mbar_arrive(&bar.t_full[st]);
                 }
             }
             if (!ok) give_up();
@@ -451,6 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int tt = r / s.G;
         uint32_t g = 0, works = 0, n = 0;
         bool ok = true;
+        const uint64_t sc2 = tc::f2_pack(a.scale_log2, a.scale_log2);
         for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
             Work k;
             if (!decode_work<MODE>(a, w, &k)) continue;
@@ -464,11 +527,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) tc::mbar_arrive(&bar.aux_empty[buf]);
                 ++n;
             }
+            const uint64_t lse2 = tc::f2_pack(-mine.x, -mine.x), del2 = tc::f2_pack(-mine.y, -mine.y);
             for (int i = 0; i < k.n; ++i, ++g) {
                 if ((int)(g & 1) != wg) continue;
                 if (!warp_wait(&bar.s_full[wg], (g >> 1) & 1)) { ok = false; break; }
-                const int st = g % L::NST;
-                if (MODE == DKV && !warp_wait(&bar.aux_full[st], (g / L::NST) & 1)) { ok = false; break; }
                 tc::fence_after_sync();
                 uint32_t x[64], y[64];
                 tc::tmem_ld32(tS, x);
@@ -491,7 +553,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                     lo = max(min(pos - tb, BN), -BN) * s.G;
                     hi = pos < s.ns ? BN - 1 : max(min(pos - tb + s.win, BN), -BN) * s.G - 1;
                 }
-                const float4* ax = reinterpret_cast<const float4*>(aux + st * BN);      // DKV: two columns each
                 tc::tmem_wait_ld();
                 const bool full = hi >= BN - 1 && (lo <= 0 || sk >= BN);
                 if (!__all_sync(0xffffffffu, full)) {
@@ -503,16 +564,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                             if (!((bits >> e) & 1u)) x[32 * c + e] = 0xFF800000u;
                     }
                 }
+                // (DKV: mine = 0, S and D carry the queries' lse and delta)
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
-                    float l0 = mine.x, l1 = mine.x;
-                    if (MODE == DKV) {
-                        const float4 v = ax[c / 2];
-                        l0 = v.x;
-                        l1 = v.z;
-                    }
-                    x[c] = __float_as_uint(tc::ex2(fmaf(__uint_as_float(x[c]), a.scale_log2, -l0)));
-                    x[c + 1] = __float_as_uint(tc::ex2(fmaf(__uint_as_float(x[c + 1]), a.scale_log2, -l1)));
+                    float y0, y1;
+                    tc::f2_unpack(tc::f2_fma(tc::f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, lse2),
+                                  y0, y1);
+                    x[c] = __float_as_uint(tc::ex2(y0));
+                    x[c + 1] = __float_as_uint(tc::ex2(y1));
                 }
                 if (!warp_wait(&bar.d_full[wg], (g >> 1) & 1)) { ok = false; break; }
                 tc::fence_after_sync();
@@ -527,15 +586,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // bf16 weights and ds: half a step, 2^-9 relative of each term
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
-                    float e0 = mine.y, e1 = mine.y;
-                    if (MODE == DKV) {
-                        const float4 v = ax[c / 2];
-                        e0 = v.y;
-                        e1 = v.w;
-                    }
-                    const float p0 = __uint_as_float(x[c]), p1 = __uint_as_float(x[c + 1]);
-                    y[c / 2] = tc::pack_bf16x2(p0 * (__uint_as_float(y[c]) - e0), p1 * (__uint_as_float(y[c + 1]) - e1));
-                    x[c / 2] = tc::pack_bf16x2(p0, p1);
+                    const uint64_t p2 = tc::f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                    const uint64_t d2 = tc::f2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1]));
+                    float e0, e1;
+                    tc::f2_unpack(tc::f2_mul(p2, MODE == DQ ? tc::f2_add(d2, del2) : d2), e0, e1);
+                    y[c / 2] = tc::pack_bf16x2(e0, e1);
+                    x[c / 2] = tc::pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
                 }
                 if (MODE == DKV) {
                     tc::tmem_st32(tS, x);
