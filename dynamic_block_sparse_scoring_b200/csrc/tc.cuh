@@ -72,6 +72,26 @@ __device__ __forceinline__ bool mbar_test(uint64_t* b, uint32_t parity) {
     return ok != 0;
 }
 
+// Three of them at once (bits 0-2): their latencies overlap.
+__device__ __forceinline__ uint32_t mbar_test3(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1, uint64_t* b2,
+                                               uint32_t p2) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q, r;\n\t.reg .b32 x, y;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "selp.u32 x, 2, 0, q;\n\t"
+        "selp.u32 y, 4, 0, r;\n\t"
+        "or.b32 %0, %0, x;\n\t"
+        "or.b32 %0, %0, y;\n\t}\n"
+        : "=&r"(r)
+        : "r"(smem_u32(b0)), "r"(p0), "r"(smem_u32(b1)), "r"(p1), "r"(smem_u32(b2)), "r"(p2)
+        : "memory");
+    return r;
+}
+
 // Waits until the phase of `b` with parity `parity` has completed.  Gives up
 // after `limit_ns` of wall time, or as soon as another role of the CTA has
 // raised `*abort`, and returns false; the caller then unwinds.

@@ -261,52 +261,56 @@ __global__ void __launch_bounds__(THREADS, 1)
                            k_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::K_OFF), 16, 1024),
                            v_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::V_OFF), CHUNK, 1024);
             auto uwait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
-            uint32_t ks = 0, kph = 0, vs0 = 0, vph0 = 0;    // stage and phase of key tile 0 / value tile 0
-            uint32_t nq = 0, np[2] = {0, 0};                // (nq: works, with bit t kept per tile)
+            uint32_t ks = 0, kph = 0, vs = 0, vph = 0;      // stage and phase of the next key / value tile
+            uint32_t nq = 0, np = 0;                        // bit t: parity of tile t's next Q, next P
             bool ok = true;
             for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
                 const Work k = decode_work(a, w);
-                int pend[2] = {-1, -1};         // key tile whose P V is still to be issued
                 bool first[2] = {true, true};
-                uint32_t vs = vs0, vph = vph0;  // of value tile j - 1
+                bool pv[2] = {false, false};    // P V of key tile j - 1 is still to be issued
                 int wp = 0;                     // width of key tile j - 1
-                for (int j = 0; ok && j <= k.n; ++j) {
+                // Per key tile j and query tile t: one look at the barriers (a wait for those
+                // that are not there yet) and one run of MMAs, P V of j - 1 and Q K^T of j.
+                for (int j = 0; j <= k.n; ++j) {
                     const int wj = j < k.n ? k.width(j) : 0;
                     const uint32_t idesc_w = tc::idesc_bf16_f32(BM, 0, false, false) | ((uint32_t)(wj >> 3) << 17);
                     const uint64_t kd = tc::desc_at(k_desc, ks * L::QC * CHUNK), vd = tc::desc_at(v_desc, vs * L::VC * CHUNK);
-                    const bool second = j > 0 && k.needs(1, j - 1);
-                    bool have_k = false, have_v = false;
+                    const bool qk[2] = {k.needs(0, j), k.needs(1, j)};
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        const bool want = k.needs(t, j), pv = pend[t] >= 0;
                         const bool last_q = j == k.e[t] - 1, last_p = j == k.e[t];
+                        const bool free_v = t == 1 || !pv[1], free_k = t == 1 || !qk[1];
                         const uint32_t acc = first[t] ? 0u : 1u;
-                        if (pv) {
-                            if (!have_v && !uwait(&bar.v_full[vs], vph)) { ok = false; break; }
-                            have_v = true;
-                            if (!uwait(&bar.p_full[t], np[t] & 1)) { ok = false; break; }
-                            tc::fence_after_sync();
-                            if (tc::elect_one()) {
+                        if (!pv[t] && !qk[t]) continue;
+                        const uint32_t want = (pv[t] ? 3u : 0u) | (qk[t] ? 4u : 0u);
+                        const uint32_t got = tc::mbar_test3(&bar.p_full[t], (np >> t) & 1, &bar.v_full[vs], vph,
+                                                            &bar.k_full[ks], kph);
+                        if (!__all_sync(0xffffffffu, (got & want) == want)) {
+                            if (pv[t] && (!uwait(&bar.v_full[vs], vph) || !uwait(&bar.p_full[t], (np >> t) & 1))) {
+                                ok = false;
+                                break;
+                            }
+                            if (qk[t] && !uwait(&bar.k_full[ks], kph)) { ok = false; break; }
+                        }
+                        if (qk[t] && first[t] && !uwait(&bar.q_full[t], (nq >> t) & 1)) { ok = false; break; }
+                        tc::fence_after_sync();
+                        const uint64_t qd = tc::desc_at(q_desc, t * L::QC * CHUNK);
+                        if (tc::elect_one()) {
+                            if (pv[t]) {
+                                if (wp == BN) {
 #pragma unroll
-                                for (int kk = 0; kk < BN / 16; ++kk)
-                                    if (kk * 16 < wp)
+                                    for (int kk = 0; kk < BN / 16; ++kk)
                                         tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
                                                    tc::desc_at(vd, kk * 2048), idesc_pv, kk > 0 ? 1u : acc);
-                                if (t == 1 || !second) tc::mma_commit(&bar.v_empty[vs]);
+                                } else {
+                                    for (int kk = 0; kk * 16 < wp; ++kk)
+                                        tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
+                                                   tc::desc_at(vd, kk * 2048), idesc_pv, kk > 0 ? 1u : acc);
+                                }
+                                if (free_v) tc::mma_commit(&bar.v_empty[vs]);
                                 if (last_p) tc::mma_commit(&bar.o_full[t]);
                             }
-                            __syncwarp();
-                            ++np[t];
-                            first[t] = false;
-                            pend[t] = -1;
-                        }
-                        if (want) {
-                            if (first[t] && !uwait(&bar.q_full[t], (nq >> t) & 1)) { ok = false; break; }
-                            if (!have_k && !uwait(&bar.k_full[ks], kph)) { ok = false; break; }
-                            have_k = true;
-                            tc::fence_after_sync();
-                            const uint64_t qd = tc::desc_at(q_desc, t * L::QC * CHUNK);
-                            if (tc::elect_one()) {
+                            if (qk[t]) {
 #pragma unroll
                                 for (int kk = 0; kk < DQK / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * CHUNK + (kk & 3) * 32;
@@ -314,24 +318,24 @@ __global__ void __launch_bounds__(THREADS, 1)
                                                kk > 0);
                                 }
                                 tc::mma_commit(&bar.s_full[t]);
+                                if (free_k) tc::mma_commit(&bar.k_empty[ks]);
                                 if (last_q) tc::mma_commit(&bar.q_empty[t]);
                             }
-                            __syncwarp();
-                            if (last_q) nq ^= 1u << t;
-                            pend[t] = j;
                         }
-                    }
-                    if (ok && j < k.n) {        // (every key tile has a query tile that needs it)
-                        if (!have_k && !uwait(&bar.k_full[ks], kph)) ok = false;
-                        if (ok && tc::elect_one()) tc::mma_commit(&bar.k_empty[ks]);
                         __syncwarp();
-                        if (++ks == L::KS) ks = 0, kph ^= 1;
+                        if (pv[t]) {
+                            np ^= 1u << t;
+                            first[t] = false;
+                        }
+                        if (last_q) nq ^= 1u << t;
                     }
+                    if (!ok) break;
                     if (j > 0 && ++vs == L::VS) vs = 0, vph ^= 1;
+                    if (j < k.n && ++ks == L::KS) ks = 0, kph ^= 1;
+                    pv[0] = qk[0];
+                    pv[1] = qk[1];
                     wp = wj;
                 }
-                vs0 = vs;
-                vph0 = vph;
             }
             if (!ok && lane == 0) give_up();
             if (tc::elect_one()) tc::mma_commit(&bar.drain);    // every MMA has completed before TMEM is freed
