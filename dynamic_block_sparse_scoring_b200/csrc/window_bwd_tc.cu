@@ -122,9 +122,15 @@ __host__ __device__ __forceinline__ void tile_queries(const WinShape& s, int u0,
 struct Work {
     int b, kvh, n;      // n: steps
     int first;          // DQ: first token of the query tile.  DKV: first key of the tile
-    int base;           // DKV: token of step 0
+    int base, rot;      // DKV: first token, and which step's place the first step takes
     int nst, sl, lo;    // DQ: sink steps, sinks before the window, first key of the window's steps
     int slot;           // DKV: partial-sum slot, -1: the only item of its key tile
+
+    // DKV: first token of step i.  The steps run backwards and turned so that CTAs whose key
+    // tiles share queries come to them at the same time: block b of tok tokens is taken at
+    // step (last block - b) mod n.  In their natural order neighbouring key tiles come to the
+    // same rows 128 tokens apart, with more than the L2's capacity read in between.
+    __device__ __forceinline__ int token(int i, int tok) const { return base + (rot >= i ? rot - i : rot - i + n) * tok; }
 };
 
 template <int MODE>
@@ -161,6 +167,7 @@ __device__ __forceinline__ bool decode_work(const Args& a, int w, Work* k) {
     if (c >= items) return false;
     k->base = i0 + c * chunk * a.tok;
     k->n = min(chunk, steps - c * chunk);
+    k->rot = k->n > 0 ? (ceil_div(s.Tq, a.tok) - 1 - k->base / a.tok) % k->n : 0;
     k->slot = items == 1 ? -1
                          : (sinks ? 0 : n_s) + (plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp + c;
     return true;
@@ -281,7 +288,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                             tc::tma_load_3d(dst + c * TCHUNK, m, &bar.t_full[st], x,
                                             i < k.nst ? i * BN : k.lo + (i - k.nst) * BN, plane);
                         else
-                            tc::tma_load_4d(dst + c * TCHUNK, m, &bar.t_full[st], x, h0, k.base + i * a.tok, k.b);
+                            tc::tma_load_4d(dst + c * TCHUNK, m, &bar.t_full[st], x, h0, k.token(i, a.tok), k.b);
+                    }
+                    // the rows after the stages' into L2 (rows outside the tensor are not fetched)
+                    if (MODE == DKV && i + 2 < k.n) {
+#pragma unroll
+                        for (int c = 0; c < L::QC + L::VC; ++c)
+                            tc::tma_prefetch_l2_4d(c < L::QC ? &map_t1 : &map_t2, 64 * (c < L::QC ? c : c - L::QC), h0,
+                                                   k.token(i + 2, a.tok), k.b);
                     }
                 }
             }
@@ -476,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     float2 v[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = lane + 32 * e, tt = r / s.G, tok = k.base + i * a.tok + tt;
+                        const int r = lane + 32 * e, tt = r / s.G, tok = k.token(i, a.tok) + tt;
                         v[e] = make_float2(-1e30f, 0.f);        // p = 0: no query
                         if (tt < a.tok && tok < s.Tq) {
                             const size_t row = ((size_t)k.b * s.Tq + tok) * s.Hq + k.kvh * s.G + (r - tt * s.G);
@@ -549,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 } else {
                     // tokens from pos on, up to pos + win - 1 unless the key is a sink
-                    const int tb = s.q0 + k.base + i * a.tok;
+                    const int tb = s.q0 + k.token(i, a.tok);
                     lo = max(min(pos - tb, BN), -BN) * s.G;
                     hi = pos < s.ns ? BN - 1 : max(min(pos - tb + s.win, BN), -BN) * s.G - 1;
                 }
