@@ -105,6 +105,7 @@ struct Args {
     int tok;            // tokens per query tile (DQ) or per step (DKV)
     int n_tt;           // query tiles per (sequence, KV head) (DQ)
     int n_work;
+    bool turned;        // DKV: see Work::token
     float scale_log2;
 };
 
@@ -126,11 +127,12 @@ struct Work {
     int nst, sl, lo;    // DQ: sink steps, sinks before the window, first key of the window's steps
     int slot;           // DKV: partial-sum slot, -1: the only item of its key tile
 
-    // DKV: first token of step i.  The steps run backwards and turned so that CTAs whose key
-    // tiles share queries come to them at the same time: block b of tok tokens is taken at
-    // step (last block - b) mod n.  In their natural order neighbouring key tiles come to the
-    // same rows 128 tokens apart, with more than the L2's capacity read in between.
-    __device__ __forceinline__ int token(int i, int tok) const { return base + (rot >= i ? rot - i : rot - i + n) * tok; }
+    // DKV: first token of step i.  Turned (rot >= 0), the steps run backwards from rot on and
+    // around, so that CTAs whose key tiles share queries come to them at the same time: block
+    // b of tok tokens is taken at step (last block - b) mod n.
+    __device__ __forceinline__ int token(int i, int tok) const {
+        return base + (rot < 0 ? i : rot >= i ? rot - i : rot - i + n) * tok;
+    }
 };
 
 template <int MODE>
@@ -167,7 +169,7 @@ __device__ __forceinline__ bool decode_work(const Args& a, int w, Work* k) {
     if (c >= items) return false;
     k->base = i0 + c * chunk * a.tok;
     k->n = min(chunk, steps - c * chunk);
-    k->rot = k->n > 0 ? (ceil_div(s.Tq, a.tok) - 1 - k->base / a.tok) % k->n : 0;
+    k->rot = a.turned && k->n > 0 ? (ceil_div(s.Tq, a.tok) - 1 - k->base / a.tok) % k->n : -1;
     k->slot = items == 1 ? -1
                          : (sinks ? 0 : n_s) + (plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp + c;
     return true;
@@ -525,6 +527,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t tD = tmem + L::D_COL + (L::ND == 2 ? wg * 64 : 0) + lane_off;
         const uint32_t tG = tmem + L::ACC_COL + lane_off;
         const int tt = r / s.G;
+        TileRows tile_rows;
+        if (MODE == DQ) tile_rows.init(r, s.G);
         uint32_t g = 0, works = 0, n = 0;
         bool ok = true;
         const uint64_t sc2 = tc::f2_pack(a.scale_log2, a.scale_log2);
@@ -624,42 +628,61 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::fence_after_sync();
             }
             // this warpgroup's 32-column pieces of the accumulator rows
-            OutRows rows;
+            auto acc_read = [&]() {                 // the next work may overwrite the accumulators
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.acc_free);
+            };
+            if (MODE == DQ) {
+                // all pieces into registers first: the next query tile's products start while
+                // they are stored
+                constexpr int PIECES = DQK / 64;
+                uint4 u[PIECES][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int rj = (r & ~3) + j;
-                if (MODE == DQ) {
-                    const int tj = rj / s.G, i = k.first + tj;
-                    rows.off[j] = tj < a.tok && i < s.Tq
-                                      ? ((long long)k.b * s.Tq + i) * s.Hq + k.kvh * s.G + (rj - tj * s.G)
-                                      : -1;
-                } else {
-                    const int u = k.first + rj;
+                for (int p = 0; p < PIECES; ++p) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tG + wg * 32 + 64 * p, o);
+                    tc::tmem_wait_ld32(o);
+                    pack32(o, s.scale, u[p]);
+                }
+                acc_read();
+                const OutRows rows = tile_rows.at(((long long)k.b * s.Tq + k.first) * s.Hq + k.kvh * s.G,
+                                                  min(a.tok, s.Tq - k.first), s.Hq);
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) store_bf16x32(u[p], a.dq, rows, DQK, wg * 32 + 64 * p, lane);
+                ++works;
+            } else {
+                OutRows rows;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int rj = (r & ~3) + j, u = k.first + rj;
                     rows.off[j] = u >= s.Tk       ? -1
                                   : k.slot >= 0 ? (long long)k.slot * BM + rj
                                                 : ((long long)k.b * s.Hkv + k.kvh) * s.Tk + u;
                 }
-            }
 #pragma unroll 1
-            for (int c = wg * 32; c < L::ACC; c += 64) {
-                uint32_t o[32];
-                if (k.n > 0) {
-                    tc::tmem_ld32(tG + c, o);
-                    tc::tmem_wait_ld32(o);
-                } else {                            // keys that no query sees
+                for (int c = wg * 32; c < L::ACC; c += 64) {
+                    uint32_t o[32];
+                    uint4 u[4];
+                    if (k.n > 0) {
+                        tc::tmem_ld32(tG + c, o);
+                        tc::tmem_wait_ld32(o);
+                    } else {                        // keys that no query sees
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
+                    if (k.slot >= 0) {
+                        store_f32x32(o, a.part, rows, L::ACC, c, lane);
+                    } else {
+                        pack32(o, c < DV ? 1.f : s.scale, u);
+                        if (c < DV) store_bf16x32(u, a.dv, rows, DV, c, lane);
+                        else store_bf16x32(u, a.dk, rows, DQK, c - DV, lane);
+                    }
                 }
-                if (MODE == DQ) store_bf16x32(o, s.scale, a.dq, rows, DQK, c, lane);
-                else if (k.slot >= 0) store_f32x32(o, a.part, rows, L::ACC, c, lane);
-                else if (c < DV) store_bf16x32(o, 1.f, a.dv, rows, DV, c, lane);
-                else store_bf16x32(o, s.scale, a.dk, rows, DQK, c - DV, lane);
-            }
-            if (k.n > 0) {
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar.acc_free);
-                ++works;
+                if (k.n > 0) {
+                    acc_read();
+                    ++works;
+                }
             }
         }
         if (!ok) give_up();
@@ -797,6 +820,11 @@ cudaError_t launch_window_bwd_tc(const WinShape& s, const __nv_bfloat16* q, cons
     a.dv = dv;
     a.part = part;
     a.tok = a.n_tt = a.n_work = 0;
+    // Neighbouring key tiles read the same rows of q and d_out.  While these fit the L2 (126 MB)
+    // beside everything else, each tile takes them in its own order (4096 tokens, 16 heads, d 128,
+    // 34 MB: 358 us a training step, 368 turned: every CTA asks for the same lines at once); larger
+    // ones would come from HBM once per key tile (8192 tokens, 64 heads, 336 MB: 1127 us, 1071 turned).
+    a.turned = (size_t)s.B * s.Tq * s.Hq * (s.dqk + s.dv) * 2 > ((size_t)64 << 20);
     a.scale_log2 = s.scale * LOG2E;
 #define NSA_WIN_CASE(A, B) \
     if (s.dqk == A && s.dv == B) return launch_impl<A, B>(a, q, k, v, st);

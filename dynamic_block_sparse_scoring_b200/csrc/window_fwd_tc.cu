@@ -350,6 +350,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + t * 128 + lane_off, tO = tmem + 256 + t * DV + lane_off;
         const int tt = r / s.G, g = r - tt * s.G;
+        TileRows tile_rows;
+        tile_rows.init(r, s.G);
         uint32_t ns = 0, no = 0;
         bool ok = true;
         auto warp_wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
@@ -460,21 +462,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!warp_wait(&bar.o_full[t], no & 1)) { ok = false; break; }
             ++no;
             tc::fence_after_sync();
-            OutRows rows;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int rj = (r & ~3) + j, tj = rj / s.G, i = (k.tt0 + t) * a.tok + tj;
-                rows.off[j] = tj < a.tok && i < s.Tq
-                                  ? ((long long)k.b * s.Tq + i) * s.Hq + k.kvh * s.G + (rj - tj * s.G)
-                                  : -1;
-            }
+            const int i0 = (k.tt0 + t) * a.tok;
+            const OutRows rows = tile_rows.at(((long long)k.b * s.Tq + i0) * s.Hq + k.kvh * s.G, min(a.tok, s.Tq - i0), s.Hq);
             const float inv = 1.f / l;
 #pragma unroll 1
             for (int c = 0; c < DV; c += 32) {
                 uint32_t o[32];
+                uint4 u[4];
                 tc::tmem_ld32(tO + c, o);
                 tc::tmem_wait_ld32(o);
-                store_bf16x32(o, inv, a.out, rows, DV, c, lane);
+                pack32(o, inv, u);
+                store_bf16x32(u, a.out, rows, DV, c, lane);
             }
             if (row_ok && a.lse)
                 a.lse[((size_t)k.b * s.Tq + (pos - s.q0)) * s.Hq + k.kvh * s.G + g] =
