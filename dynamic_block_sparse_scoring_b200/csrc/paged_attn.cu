@@ -33,7 +33,7 @@ namespace {
 constexpr int TILE = 16;                // keys per tile
 constexpr int ROWS = 16;                // query rows per unit
 constexpr int KST = 3, VST = 2;         // ring stages of a worker
-constexpr int MIN_TILES = 4;            // least share of a worker
+constexpr int MIN_TILES = 2;            // least share of a worker
 
 template <int DQK, int DV>
 struct Dim {
@@ -395,48 +395,46 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
     }
 }
 
-// Joins the shares of one (unit, row): warp w takes the shares w, w + 4, ...;
-// units without keys get 0 and -inf.
+// Joins the shares of a unit's rows; units without keys get 0 and -inf.  A warp
+// has a row (blockIdx.y: four rows), or, with fewer than four rows (one query
+// head per KV head), the four warps have one row's shares w, w + 4, ...: such
+// units are few and their shares many.
 constexpr int JOIN_WARPS = 4;
 
-template <int DV>
+template <int DV, bool SPLIT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const PagedArgs a, int workers) {
     constexpr int NC = DV / 64;                     // column pairs per lane
-    __shared__ float2 acc_s[JOIN_WARPS][DV / 2];
+    __shared__ float2 acc_s[SPLIT ? JOIN_WARPS : 1][SPLIT ? DV / 2 : 1];
     const PagedShape& s = a.s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per_seq = s.Hkv * a.RT;
     const int b = blockIdx.x / per_seq, unit = blockIdx.x % per_seq;
-    const int h = unit / a.RT, rt = unit % a.RT, r = rt * ROWS + blockIdx.y;
-    if (r >= s.Tq * s.G) return;
-    const size_t orow = ((size_t)b * s.Tq + r / s.G) * s.Hq + h * s.G + r % s.G;
+    const int h = unit / a.RT, rt = unit % a.RT;
+    const int ru = SPLIT ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;     // row of the unit
+    const int r = rt * ROWS + ru;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (r >= s.Tq * s.G) return;                    // (whole CTAs when SPLIT)
+    const size_t orow = ((size_t)b * s.Tq + r / s.G) * s.Hq + h * s.G + r % s.G;
     const long long p0 = a.prefix[b], n = (a.prefix[b + 1] - p0) / per_seq;
-    if (n == 0) {
-        for (int c = threadIdx.x; c < DV / 2; c += JOIN_WARPS * 32)
-            reinterpret_cast<uint32_t*>(a.out + orow * DV)[c] = 0u;
-        if (a.lse && threadIdx.x == 0) a.lse[orow] = -INFINITY;
-        return;
-    }
     const long long per = share_of(a.prefix[s.B], workers);
     const long long first = p0 + unit * n, last = first + n - 1;
-    const int w0 = (int)(first / per), w1 = (int)(last / per);
-    if (w0 == w1) return;                           // finished by its worker
+    const int w0 = (int)(first / per), w1 = n > 0 ? (int)(last / per) : w0 - 1;
+    if (n > 0 && w0 == w1) return;                  // finished by its worker
     auto part_row = [&](int w) {                    // only w0 starts the unit
-        return (size_t)(2 * w + (w == w0 ? 1 : 0)) * ROWS + blockIdx.y;
+        return (size_t)(2 * w + (w == w0 ? 1 : 0)) * ROWS + ru;
     };
     float mx = -INFINITY;
     for (int w = w0 + lane; w <= w1; w += 32) mx = fmaxf(mx, a.part_lse[part_row(w)]);
     mx = warp_max(mx);
     const float ref = mx == -INFINITY ? 0.f : mx;
     float sum = 0.f;
-    for (int w = w0 + lane; w <= w1; w += 32) sum += tc::ex2(a.part_lse[part_row(w)] - ref);
-    sum = warp_sum(sum);
     float2 acc[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[c] = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int w = w0 + warp; w <= w1; w += JOIN_WARPS) {
+    for (int w = w0 + lane; w <= w1; w += 32) sum += tc::ex2(a.part_lse[part_row(w)] - ref);
+    sum = warp_sum(sum);
+#pragma unroll 8
+    for (int w = w0 + (SPLIT ? warp : 0); w <= w1; w += SPLIT ? JOIN_WARPS : 1) {
         const size_t pr = part_row(w);
         const float wt = tc::ex2(a.part_lse[pr] - ref);
 #pragma unroll
@@ -445,20 +443,26 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const Paged
             acc[c] = make_float2(fmaf(wt, x.x, acc[c].x), fmaf(wt, x.y, acc[c].y));
         }
     }
-#pragma unroll
-    for (int c = 0; c < NC; ++c) acc_s[warp][c * 32 + lane] = acc[c];
-    __syncthreads();
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    for (int c = threadIdx.x; c < DV / 2; c += JOIN_WARPS * 32) {
-        float x = 0.f, y = 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * DV);
+    if (SPLIT) {
 #pragma unroll
-        for (int w = 0; w < JOIN_WARPS; ++w) {
-            x += acc_s[w][c].x;
-            y += acc_s[w][c].y;
+        for (int c = 0; c < NC; ++c) acc_s[warp][c * 32 + lane] = acc[c];
+        __syncthreads();
+        for (int c = threadIdx.x; c < DV / 2; c += JOIN_WARPS * 32) {
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int w = 0; w < JOIN_WARPS; ++w) {
+                x += acc_s[w][c].x;
+                y += acc_s[w][c].y;
+            }
+            dst[c] = tc::pack_bf16x2(x * inv, y * inv);
         }
-        reinterpret_cast<uint32_t*>(a.out + orow * DV)[c] = tc::pack_bf16x2(x * inv, y * inv);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) dst[c * 32 + lane] = tc::pack_bf16x2(acc[c].x * inv, acc[c].y * inv);
     }
-    if (a.lse && threadIdx.x == 0)
+    if (a.lse && lane == 0 && (!SPLIT || warp == 0))
         a.lse[orow] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -481,7 +485,8 @@ cudaError_t launch_impl(PagedArgs a, int n_units, int rows, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(n_units, std::min(rows, ROWS));
+    const bool split = rows < JOIN_WARPS;
+    cfg.gridDim = dim3(n_units, split ? rows : (std::min(rows, ROWS) + JOIN_WARPS - 1) / JOIN_WARPS);
     cfg.blockDim = dim3(JOIN_WARPS * 32);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -489,7 +494,8 @@ cudaError_t launch_impl(PagedArgs a, int n_units, int rows, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<DV>, a, grid * L::WARPS);
+    return cudaLaunchKernelEx(&cfg, split ? paged_join_kernel<DV, true> : paged_join_kernel<DV, false>, a,
+                              grid * L::WARPS);
 }
 
 }  // namespace

@@ -52,7 +52,7 @@ constexpr int RCHUNK = 16384, TCHUNK = 8192;    // 128 / 64 rows x 64 columns of
 constexpr int THREADS = 384;
 constexpr uint64_t WAIT_NS = 1000000000ull;
 constexpr int SMS = 148;                        // the split of key tiles is planned for this many SMs
-constexpr int MIN_CHUNK = 8;                    // least steps of an item of a split key tile
+constexpr int MIN_CHUNK = 4;                    // least steps of an item of a split key tile
 constexpr float LOG2E = 1.4426950408889634f;
 
 enum { DQ = 0, DKV = 1 };
