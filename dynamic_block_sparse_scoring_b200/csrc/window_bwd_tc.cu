@@ -529,17 +529,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int tt = r / s.G;
         TileRows tile_rows;
         if (MODE == DQ) tile_rows.init(r, s.G);
-        constexpr int PIECES = MODE == DQ ? DQK / 64 : 1;
-        uint4 held[PIECES][4];                      // DQ: this lane's pieces of the last query tile's dq
-        long long held_base = 0;
-        int held_tokens = 0;
-        auto store_held = [&]() {
-            if (held_tokens == 0) return;
-            const OutRows rows = tile_rows.at(held_base, held_tokens, s.Hq);
-#pragma unroll
-            for (int p = 0; p < PIECES; ++p) store_bf16x32(held[p], a.dq, rows, DQK, wg * 32 + 64 * p, lane);
-            held_tokens = 0;
-        };
         uint32_t g = 0, works = 0, n = 0;
         bool ok = true;
         const uint64_t sc2 = tc::f2_pack(a.scale_log2, a.scale_log2);
@@ -632,10 +621,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bar.p_full[wg]);
-                if (MODE == DQ) store_held();
             }
             if (!ok) break;
-            if (MODE == DQ) store_held();           // (a query tile of one step leaves a warpgroup none)
             if (k.n > 0) {
                 if (!warp_wait(&bar.acc_full, works & 1)) { ok = false; break; }
                 tc::fence_after_sync();
@@ -647,18 +634,22 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) tc::mbar_arrive(&bar.acc_free);
             };
             if (MODE == DQ) {
-                // all pieces into registers; they are stored behind the next query tile's first
-                // step, which the tensor cores wait for
+                // all pieces into registers first: the next query tile's products start while
+                // they are stored
+                constexpr int PIECES = DQK / 64;
+                uint4 u[PIECES][4];
 #pragma unroll
                 for (int p = 0; p < PIECES; ++p) {
                     uint32_t o[32];
                     tc::tmem_ld32(tG + wg * 32 + 64 * p, o);
                     tc::tmem_wait_ld32(o);
-                    pack32(o, s.scale, held[p]);
+                    pack32(o, s.scale, u[p]);
                 }
                 acc_read();
-                held_base = ((long long)k.b * s.Tq + k.first) * s.Hq + k.kvh * s.G;
-                held_tokens = min(a.tok, s.Tq - k.first);
+                const OutRows rows = tile_rows.at(((long long)k.b * s.Tq + k.first) * s.Hq + k.kvh * s.G,
+                                                  min(a.tok, s.Tq - k.first), s.Hq);
+#pragma unroll
+                for (int p = 0; p < PIECES; ++p) store_bf16x32(u[p], a.dq, rows, DQK, wg * 32 + 64 * p, lane);
                 ++works;
             } else {
                 OutRows rows;
@@ -694,7 +685,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
         }
-        if (MODE == DQ) store_held();
         if (!ok) give_up();
     }
     tc::fence_before_sync();
