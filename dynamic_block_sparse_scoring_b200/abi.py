@@ -421,32 +421,33 @@ def _device(*named):
     if dev.type != "cuda":
         raise ValueError(f"{named[0][0]} is on {dev}: all tensors belong on one CUDA device")
     for name, t, shape, dtype in named:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            continue
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}: all tensors belong on one CUDA device")
         if t.dtype != dtype or t.shape != shape:
             raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}: expected {dtype} {tuple(shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} is not contiguous")
+        raise ValueError(f"{name} is not contiguous")
     return dev
 
 
-def _run(fn, dev, cfg, *args):
-    """Calls an entry point with cfg, the given tensors, sizes and Nones, and dev's current stream;
-    dev becomes the current device for the call where it is not."""
-    if torch.cuda.current_device() != dev.index:
+def _run(fn, dev, *args):
+    """Calls an entry point with the given arguments and dev's current stream; dev becomes the
+    current device for the call where it is not."""
+    if torch._C._cuda_getDevice() != dev.index:
         with torch.cuda.device(dev):
-            return _run(fn, dev, cfg, *args)
-    status = getattr(lib, fn)(cfg, *[a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args],
-                              torch._C._cuda_getCurrentRawStream(dev.index))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if status != 0:
-        raise NsaError(fn, status)
+        raise NsaError(fn.__name__, status)
 
 
 def _size(fn, cfg) -> int:
     n = _sz(0)
-    status = getattr(lib, fn)(cfg, n)
+    status = fn(cfg, n)
     if status != 0:
-        raise NsaError(fn, status)
+        raise NsaError(fn.__name__, status)
     return n.value
 
 
@@ -455,26 +456,28 @@ _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 def window_forward(cfg: NsaWindowConfig, q, k, v):
     """Window attention with sink tokens on the current stream: (out bf16, lse fp32)."""
-    B, Tq, Hq, Tk = cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.seqlen_kv
-    dev = _device(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), ("k", k, (B, cfg.h_kv, Tk, cfg.d_qk), _BF16),
-                  ("v", v, (B, cfg.h_kv, Tk, cfg.d_v), _BF16))
-    out = torch.empty((B, Tq, Hq, cfg.d_v), dtype=_BF16, device=dev)
-    lse = torch.empty((B, Tq, Hq), dtype=_F32, device=dev)
-    _run("nsa_window_attn_fwd", dev, cfg, q, k, v, out, lse)
+    B, Tq, Hq, Hkv, Tk, d, dv = (cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.h_kv, cfg.seqlen_kv, cfg.d_qk, cfg.d_v)
+    dev = _device(("q", q, (B, Tq, Hq, d), _BF16), ("k", k, (B, Hkv, Tk, d), _BF16),
+                  ("v", v, (B, Hkv, Tk, dv), _BF16))
+    out = q.new_empty((B, Tq, Hq, dv))
+    lse = q.new_empty((B, Tq, Hq), dtype=_F32)
+    _run(lib.nsa_window_attn_fwd, dev, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+         lse.data_ptr())
     return out, lse
 
 
 def window_backward(cfg: NsaWindowConfig, q, k, v, out, lse, d_out):
     """Gradients (dq, dk, dv), bf16, of window_forward on the current stream."""
-    B, Tq, Hq, Tk = cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.seqlen_kv
-    o_shape = (B, Tq, Hq, cfg.d_v)
-    dev = _device(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), ("k", k, (B, cfg.h_kv, Tk, cfg.d_qk), _BF16),
-                  ("v", v, (B, cfg.h_kv, Tk, cfg.d_v), _BF16), ("out", out, o_shape, _BF16),
+    B, Tq, Hq, Hkv, Tk, d, dv = (cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.h_kv, cfg.seqlen_kv, cfg.d_qk, cfg.d_v)
+    o_shape = (B, Tq, Hq, dv)
+    dev = _device(("q", q, (B, Tq, Hq, d), _BF16), ("k", k, (B, Hkv, Tk, d), _BF16),
+                  ("v", v, (B, Hkv, Tk, dv), _BF16), ("out", out, o_shape, _BF16),
                   ("lse", lse, (B, Tq, Hq), _F32), ("d_out", d_out, o_shape, _BF16))
-    n = _size("nsa_window_bwd_workspace_size", cfg)
+    n = _size(lib.nsa_window_bwd_workspace_size, cfg)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws = torch.empty(n, dtype=_U8, device=dev)
-    _run("nsa_window_attn_bwd", dev, cfg, q, k, v, out, lse, d_out, dq, dk, dv, ws, n)
+    ws = q.new_empty(n, dtype=_U8)
+    _run(lib.nsa_window_attn_bwd, dev, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+         lse.data_ptr(), d_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), n)
     return dq, dk, dv
 
 
@@ -495,11 +498,12 @@ def paged_attention(cfg: NsaPagedConfig, q, k_pages, v_pages, table, lens):
     B, Tq, Hq = cfg.batch, cfg.seqlen_q, cfg.h_q
     dev = _device(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), *_cache(cfg, k_pages, v_pages),
                   *_books(cfg, table, lens))
-    n = _size("nsa_paged_workspace_size", cfg)
-    out = torch.empty((B, Tq, Hq, cfg.d_v), dtype=_BF16, device=dev)
-    lse = torch.empty((B, Tq, Hq), dtype=_F32, device=dev)
-    ws = torch.empty(n, dtype=_U8, device=dev)
-    _run("nsa_paged_attn_fwd", dev, cfg, q, k_pages, v_pages, table, lens, out, lse, ws, n)
+    n = _size(lib.nsa_paged_workspace_size, cfg)
+    out = q.new_empty((B, Tq, Hq, cfg.d_v))
+    lse = q.new_empty((B, Tq, Hq), dtype=_F32)
+    ws = q.new_empty(n, dtype=_U8)
+    _run(lib.nsa_paged_attn_fwd, dev, cfg, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+         table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), n)
     return out, lse
 
 
@@ -510,10 +514,12 @@ def paged_append(cfg: NsaPagedConfig, k_new, v_new, k_pages, v_pages, table, len
     extra = () if n_new is None else (("n_new", n_new, (cfg.batch,), _I32),)
     dev = _device(("k_new", k_new, new + (cfg.d_qk,), _BF16), ("v_new", v_new, new + (cfg.d_v,), _BF16),
                   *_cache(cfg, k_pages, v_pages), *_books(cfg, table, lens, ref), *extra)
-    n = _size("nsa_paged_append_workspace_size", cfg)
-    short = torch.empty(1, dtype=_I32, device=dev)
-    ws = torch.empty(n, dtype=_U8, device=dev)
-    _run("nsa_paged_append", dev, cfg, k_new, v_new, n_new, k_pages, v_pages, table, lens, ref, short, ws, n)
+    n = _size(lib.nsa_paged_append_workspace_size, cfg)
+    short = lens.new_empty(1)
+    ws = lens.new_empty(n, dtype=_U8)
+    _run(lib.nsa_paged_append, dev, cfg, k_new.data_ptr(), v_new.data_ptr(),
+         None if n_new is None else n_new.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+         table.data_ptr(), lens.data_ptr(), ref.data_ptr(), short.data_ptr(), ws.data_ptr(), n)
     return short
 
 
@@ -521,8 +527,9 @@ def pages_fork(cfg: NsaPagedConfig, src, dst, table, lens, ref):
     """Rows dst share the pages of rows src; returns done [n] int32 (1: carried out)."""
     n = src.numel()
     dev = _device(("src", src, (n,), _I32), ("dst", dst, (n,), _I32), *_books(cfg, table, lens, ref))
-    done = torch.empty(n, dtype=_I32, device=dev)
-    _run("nsa_pages_fork", dev, cfg, n, src, dst, table, lens, ref, done)
+    done = torch.empty_like(src)
+    _run(lib.nsa_pages_fork, dev, cfg, n, src.data_ptr(), dst.data_ptr(), table.data_ptr(), lens.data_ptr(),
+         ref.data_ptr(), done.data_ptr())
     return done
 
 
@@ -531,17 +538,18 @@ def pages_free(cfg: NsaPagedConfig, rows, table, lens, ref, keep=None):
     n = rows.numel()
     extra = () if keep is None else (("keep", keep, (n,), _I32),)
     dev = _device(("rows", rows, (n,), _I32), *_books(cfg, table, lens, ref), *extra)
-    done = torch.empty(n, dtype=_I32, device=dev)
-    _run("nsa_pages_free", dev, cfg, n, rows, keep, table, lens, ref, done)
+    done = torch.empty_like(rows)
+    _run(lib.nsa_pages_free, dev, cfg, n, rows.data_ptr(), None if keep is None else keep.data_ptr(),
+         table.data_ptr(), lens.data_ptr(), ref.data_ptr(), done.data_ptr())
     return done
 
 
 def pages_compact(cfg: NsaPagedConfig, k_pages, v_pages, table, lens, ref):
     """Moves the pages in use to the lowest ids, in place; returns (remap [n_pages], n_live [1])."""
     dev = _device(*_cache(cfg, k_pages, v_pages), *_books(cfg, table, lens, ref))
-    n = _size("nsa_pages_compact_workspace_size", cfg)
-    remap = torch.empty(cfg.n_pages, dtype=_I32, device=dev)
-    n_live = torch.empty(1, dtype=_I32, device=dev)
-    ws = torch.empty(n, dtype=_U8, device=dev)
-    _run("nsa_pages_compact", dev, cfg, k_pages, v_pages, table, lens, ref, remap, n_live, ws, n)
+    n = _size(lib.nsa_pages_compact_workspace_size, cfg)
+    remap, n_live = torch.empty_like(ref), lens.new_empty(1)
+    ws = lens.new_empty(n, dtype=_U8)
+    _run(lib.nsa_pages_compact, dev, cfg, k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(),
+         lens.data_ptr(), ref.data_ptr(), remap.data_ptr(), n_live.data_ptr(), ws.data_ptr(), n)
     return remap, n_live
