@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
     __shared__ long long wsum[L::WARPS];
     const PagedShape& s = a.s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_launch();
 
     // first tile of every sequence: thread i sums the chunk of sequences
     // [i C, (i + 1) C), the block scans the sums
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const Paged
     const int h = unit / a.RT, rt = unit % a.RT;
     const int ru = SPLIT ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;     // row of the unit
     const int r = rt * ROWS + ru;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_wait();
     if (r >= s.Tq * s.G) return;                    // (whole CTAs when SPLIT)
     const size_t orow = ((size_t)b * s.Tq + r / s.G) * s.Hq + h * s.G + r % s.G;
     const long long p0 = a.prefix[b], n = (a.prefix[b + 1] - p0) / per_seq;
@@ -484,18 +484,10 @@ cudaError_t launch_impl(PagedArgs a, int n_units, int rows, cudaStream_t st) {
     paged_attn_kernel<DQK, DV><<<grid, L::WARPS * 32, L::SMEM, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
     const bool split = rows < JOIN_WARPS;
-    cfg.gridDim = dim3(n_units, split ? rows : (std::min(rows, ROWS) + JOIN_WARPS - 1) / JOIN_WARPS);
-    cfg.blockDim = dim3(JOIN_WARPS * 32);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, split ? paged_join_kernel<DV, true> : paged_join_kernel<DV, false>, a,
-                              grid * L::WARPS);
+    const dim3 join_grid(n_units, split ? rows : (std::min(rows, ROWS) + JOIN_WARPS - 1) / JOIN_WARPS);
+    return launch_dependent(split ? paged_join_kernel<DV, true> : paged_join_kernel<DV, false>, join_grid,
+                            JOIN_WARPS * 32, 0, st, a, grid * L::WARPS);
 }
 
 }  // namespace

@@ -18,9 +18,6 @@ namespace {
 
 constexpr int PLAN_THREADS = 1024;
 
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Exclusive scan of x over the CTA's 1024 threads; *total receives the sum.
 __device__ __forceinline__ int block_scan(int x, int* total, int* warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -355,20 +352,6 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const CompactArgs a) 
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <class Args>
-cudaError_t launch_dependent(void (*kernel)(Args), dim3 grid, int threads, const Args& a, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
 }  // namespace
 
 size_t paged_append_ws_bytes(const PagedShape& s) {
@@ -392,7 +375,7 @@ cudaError_t launch_paged_append(const PagedShape& s, const __nv_bfloat16* k_new,
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int touched = (s.Tq + 2 * s.P - 2) / s.P;      // pages that Tq tokens can lie in
-    return launch_dependent(append_write_kernel, dim3(touched, s.Hkv, s.B), 256, a, st);
+    return launch_dependent(append_write_kernel, dim3(touched, s.Hkv, s.B), 256, 0, st, a);
 }
 
 cudaError_t launch_pages_fork(const PagedShape& s, int n, const int32_t* src, const int32_t* dst, int32_t* table,
@@ -419,7 +402,7 @@ cudaError_t launch_pages_compact(const PagedShape& s, __nv_bfloat16* kp, __nv_bf
     compact_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_dependent(compact_move_kernel, dim3(148 * 8), 256, a, st);
+    return launch_dependent(compact_move_kernel, dim3(148 * 8), 256, 0, st, a);
 }
 
 }  // namespace nsa

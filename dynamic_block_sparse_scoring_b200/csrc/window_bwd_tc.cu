@@ -199,6 +199,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     volatile int* abort_flag = &bar.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WinShape& s = a.s;
+    // What follows in the stream may start on the SMs that this grid leaves idle: of its
+    // results the DKV kernel reads delta alone, and waits for it.
+    pdl_launch();
 
     if (threadIdx.x == 0) {
         tc::mbar_init(&bar.r_full, 1);
@@ -475,6 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // three bf16 (24 bits), against the residents' (1, 1, 1, 0, ..).  S and D then come
             // as q.k - lse / scale and do.v - delta, and the threads, whose columns the
             // queries are, need no other value of theirs.
+            pdl_wait();                             // delta
             uint32_t g = 0;
             bool ok = true;
             const float inv_scale = 1.f / s.scale;
@@ -708,6 +712,7 @@ __global__ void __launch_bounds__(JROWS*(DQK + DV) / 4) window_bwd_join_kernel(c
     int i0, i1;
     tile_queries(s, kt * BM, &i0, &i1);
     const int items = ceil_div(ceil_div(i1 - i0, a.tok), sinks ? a.p.chunk_s : a.p.chunk_o);
+    pdl_wait();
     if (items <= 1) return;
     const int tiles = sinks ? a.p.nsk : a.p.nk - a.p.nsk, sp = sinks ? a.p.sp_s : a.p.sp_o;
     const size_t slot = (sinks ? 0 : n_s) + (size_t)(plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp;
@@ -788,13 +793,11 @@ cudaError_t launch_impl(Args a, const __nv_bfloat16* q, const __nv_bfloat16* k, 
     if (e != cudaSuccess) return e;
     a.tok = tok_s;
     a.n_work = planes * (a.p.nsk * a.p.sp_s + (a.p.nk - a.p.nsk) * a.p.sp_o);
-    kernel<<<std::min(a.n_work, nsm), THREADS, L::ALLOC, st>>>(k128, v128, q64, do64, a);
-    e = cudaGetLastError();
+    e = launch_dependent(kernel, dim3(std::min(a.n_work, nsm)), THREADS, L::ALLOC, st, k128, v128, q64, do64, a);
     if (e != cudaSuccess || (a.p.sp_s <= 1 && a.p.sp_o <= 1)) return e;
     const int tiles = a.p.sp_o > 1 ? a.p.nk : a.p.nsk;
-    window_bwd_join_kernel<DQK, DV>
-        <<<dim3(tiles * planes, BM / JROWS), JROWS * (DQK + DV) / 4, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(window_bwd_join_kernel<DQK, DV>, dim3(tiles * planes, BM / JROWS), JROWS * (DQK + DV) / 4, 0,
+                            st, a);
 }
 
 }  // namespace
