@@ -1,5 +1,4 @@
 // C ABI of the paged key/value cache: host-side validation (include/nsa.h).
-#include <math.h>
 #include <stdint.h>
 
 #include "abi_checks.cuh"
@@ -18,7 +17,7 @@ nsa_status make_paged_shape(const nsa_paged_config* cfg, PagedShape* s) {
     if (c.batch < 1 || c.seqlen_q < 1 || c.n_pages < 1 || c.max_pages < 1) return NSA_ERR_INVALID_ARG;
     if (c.h_q < 1 || c.h_kv < 1 || c.h_q % c.h_kv != 0) return NSA_ERR_INVALID_ARG;
     if (c.d_qk < 1 || c.d_v < 1 || c.page_size < 1 || c.window < 0 || c.sink < 0) return NSA_ERR_INVALID_ARG;
-    if (!isfinite(c.scale) || !(c.scale > 0.f)) return NSA_ERR_INVALID_ARG;
+    if (!(c.scale >= 1e-30f && c.scale <= 1e30f)) return NSA_ERR_INVALID_ARG;       // (NaN too)
     if (!nsa::supported_dqk(c.d_qk) || !nsa::supported_dv(c.d_v)) return NSA_ERR_UNSUPPORTED;
     int log_p = 4;
     while (log_p < 8 && (1 << log_p) != c.page_size) ++log_p;

@@ -1,6 +1,5 @@
 // C ABI of the sliding-window attention with sink tokens: host-side validation
 // and the choice of kernel (include/nsa.h).
-#include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -22,7 +21,7 @@ nsa_status make_win_shape(const nsa_window_config* cfg, WinShape* s) {
     if ((int64_t)c.q_pos0 + c.seqlen_q > c.seqlen_kv) return NSA_ERR_INVALID_ARG;
     if (c.h_q < 1 || c.h_kv < 1 || c.h_q % c.h_kv != 0) return NSA_ERR_INVALID_ARG;
     if (c.d_qk < 1 || c.d_v < 1 || c.window < 1 || c.sink < 0) return NSA_ERR_INVALID_ARG;
-    if (!isfinite(c.scale) || !(c.scale > 0.f)) return NSA_ERR_INVALID_ARG;
+    if (!(c.scale >= 1e-30f && c.scale <= 1e30f)) return NSA_ERR_INVALID_ARG;       // (NaN too)
     if (!nsa::supported_dqk(c.d_qk) || !nsa::supported_dv(c.d_v)) return NSA_ERR_UNSUPPORTED;
     // rows and planes are counted in 32 bits, and positions a tile behind the last one exist
     if ((int64_t)c.batch * c.seqlen_q * c.h_q > INT32_MAX || (int64_t)c.batch * c.h_kv * c.seqlen_kv > INT32_MAX ||

@@ -89,6 +89,7 @@ struct Split {
     int nk, nsk;        // key tiles, those with sinks
     int chunk_s, chunk_o;   // steps per item
     int sp_s, sp_o;     // most items of a key tile
+    int slots_s;        // partial-sum slots of the key tiles with sinks (0 if they are whole)
 };
 
 struct Args {
@@ -171,7 +172,7 @@ __device__ __forceinline__ bool decode_work(const Args& a, int w, Work* k) {
     k->n = min(chunk, steps - c * chunk);
     k->rot = a.turned && k->n > 0 ? (ceil_div(s.Tq, a.tok) - 1 - k->base / a.tok) % k->n : -1;
     k->slot = items == 1 ? -1
-                         : (sinks ? 0 : n_s) + (plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp + c;
+                         : (sinks ? 0 : a.p.slots_s) + (plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp + c;
     return true;
 }
 
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = lane + 32 * e, tt = r / s.G, tok = k.token(i, a.tok) + tt;
-                        v[e] = make_float2(-1e30f, 0.f);        // p = 0: no query
+                        v[e] = make_float2(-3e38f, 0.f);        // p = 0: no query
                         if (tt < a.tok && tok < s.Tq) {
                             const size_t row = ((size_t)k.b * s.Tq + tok) * s.Hq + k.kvh * s.G + (r - tt * s.G);
                             v[e] = make_float2(-a.lse[row] * inv_scale, -a.delta[row]);
@@ -706,7 +707,6 @@ __global__ void __launch_bounds__(JROWS*(DQK + DV) / 4) window_bwd_join_kernel(c
     constexpr int C4 = (DQK + DV) / 4;
     const WinShape& s = a.s;
     const int planes = s.B * s.Hkv;
-    const int n_s = planes * a.p.nsk * a.p.sp_s;
     const int plane = blockIdx.x % planes, kt = blockIdx.x / planes;
     const bool sinks = kt < a.p.nsk;
     int i0, i1;
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(JROWS*(DQK + DV) / 4) window_bwd_join_kernel(c
     pdl_wait();
     if (items <= 1) return;
     const int tiles = sinks ? a.p.nsk : a.p.nk - a.p.nsk, sp = sinks ? a.p.sp_s : a.p.sp_o;
-    const size_t slot = (sinks ? 0 : n_s) + (size_t)(plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp;
+    const size_t slot = (sinks ? 0 : a.p.slots_s) + (size_t)(plane * tiles + kt - (sinks ? 0 : a.p.nsk)) * sp;
     const int r = blockIdx.y * JROWS + threadIdx.x / C4, c = (threadIdx.x % C4) * 4;
     const int u = kt * BM + r;
     if (u >= s.Tk) return;
@@ -748,13 +748,14 @@ Split make_split(const WinShape& s) {
     p.chunk_o = std::max(1, planes * others >= 2 * SMS ? n_o : std::min(half, n_o));
     p.sp_s = ceil_div(n_s, p.chunk_s);
     p.sp_o = ceil_div(n_o, p.chunk_o);
+    p.slots_s = p.sp_s > 1 ? (int)(planes * p.nsk * p.sp_s) : 0;
     return p;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t part_slots(const WinShape& s, const Split& p) {
-    return (size_t)s.B * s.Hkv * ((size_t)p.nsk * p.sp_s + (p.sp_o > 1 ? (size_t)(p.nk - p.nsk) * p.sp_o : 0));
+    return (size_t)p.slots_s + (p.sp_o > 1 ? (size_t)s.B * s.Hkv * (p.nk - p.nsk) * p.sp_o : 0);
 }
 
 template <int DQK, int DV>

@@ -336,7 +336,7 @@ typedef struct {
     int32_t d_v;         /* value head dimension: 64, 128 or 256 */
     int32_t window;      /* keys [t - window + 1, t]; >= 1 */
     int32_t sink;        /* leading tokens that stay visible; >= 0 */
-    float scale;         /* logit scale, > 0, normally 1/sqrt(d_qk) */
+    float scale;         /* logit scale, 1e-30 .. 1e30, normally 1/sqrt(d_qk) */
     uint32_t flags;      /* 0 */
 } nsa_window_config;
 
@@ -406,7 +406,7 @@ typedef struct {
     int32_t max_pages;   /* columns of the table */
     int32_t window;      /* attention: keys [t - window + 1, t]; 0: every key up to t */
     int32_t sink;        /* attention: leading tokens that stay visible; >= 0 */
-    float scale;         /* logit scale, > 0 */
+    float scale;         /* logit scale, 1e-30 .. 1e30 */
     uint32_t flags;      /* 0 */
 } nsa_paged_config;
 

@@ -267,3 +267,51 @@ def test_a_captured_step_serves_a_growing_cache():
         assert int(short) == 0 and c.append(kn, vn, [1, 1, 1]) == 0
         c.assert_equal(x, f"step {step}")
         check_attn(cfg, c, q, out, lse, f"step {step}")
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^31 elements whose last pages are in use: attention, append, compaction."""
+    n_pages, page, h, d = 70000, 64, 4, 128
+    c = filled(2, 6, 12, page, h, d, d, [200, 130], seed=6)
+    x = c.on_gpu()
+    kp = torch.full((n_pages, h, page, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    vp = torch.full((n_pages, h, page, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    assert kp.numel() > 1 << 31
+    off = n_pages - 12
+    kp[off:], vp[off:] = x["k_pages"], x["v_pages"]
+    table = torch.where(x["table"] >= 0, x["table"] + off, x["table"])
+    ref = torch.ones(n_pages, dtype=torch.int32, device="cuda")        # the others are held elsewhere
+    ref[off:] = x["ref"]
+    lens = x["lens"].clone()
+    cfg = abi.paged_config(2, 1, 8, h, d, d, page, n_pages, 6)
+    q = torch.randn(2, 1, 8, d, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    out, lse = abi.paged_attention(cfg, q, kp, vp, table, lens)
+    check_attn(cfg, c, q, out, lse, "far pages")
+    k_new, v_new = c.new_tokens(2, 70)
+    grow = abi.paged_config(2, 70, 8, h, d, d, page, n_pages, 6)
+    assert int(abi.paged_append(grow, k_new.cuda(), v_new.cuda(), kp, vp, table, lens, ref)) == 0
+    assert c.append(k_new, v_new, [70, 70]) == 0
+    ref[:off] = 0                                                      # now the pool's beginning is free
+    remap, n_live = abi.pages_compact(cfg, kp, vp, table, lens, ref)
+    assert int(n_live) == sum(n > 0 for n in c.ref) and int(table.max()) < int(n_live)
+    out, lse = abi.paged_attention(cfg, q, kp, vp, table, lens)
+    check_attn(cfg, c, q, out, lse, "after the compaction")
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    """Calls that overlap on two streams, each with its own outputs and workspace."""
+    made = [make_attn(n, seed=7) for n in ("gqa16_192", "window_sinks")]
+    xs = [c.on_gpu() for _, c, _ in made]
+    want = [abi.paged_attention(cfg, q, x["k_pages"], x["v_pages"], x["table"], x["lens"])
+            for (cfg, _, q), x in zip(made, xs)]
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, ((cfg, _, q), x) in enumerate(zip(made, xs)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(abi.paged_attention(cfg, q, x["k_pages"], x["v_pages"], x["table"], x["lens"]))
+    torch.cuda.synchronize()
+    for w, many in zip(want, got):
+        for o, l in many:
+            assert torch.equal(o, w[0]) and torch.equal(l, w[1])

@@ -68,6 +68,22 @@ def test_large_scores(name):
         check(got, ref[n], f"{name} {n}")
 
 
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 3.0])
+def test_other_scales(scale):
+    """A scale so small that every weight is equal, and one that makes the softmax sharp; 21 tokens of
+    three heads leave rows of the streamed tiles without a query."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, d_out = r(1, 85, 6, 64), r(1, 2, 85, 64), r(1, 2, 85, 64), r(1, 85, 6, 64)
+    cfg = abi.window_config(1, 85, 85, 6, 2, 64, 64, 30, 3, scale=scale)
+    out, lse = abi.window_forward(cfg, q, k, v)
+    grads = abi.window_backward(cfg, q, k, v, out, lse, d_out)
+    ref = window_ref(q, k, v, visible(85, 85, 0, 30, 3, "cuda"), cfg.scale, d_out)
+    for n, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse) + grads):
+        check(got, ref[n], n)
+
+
 def test_lse_is_optional_and_calls_repeat_bit_for_bit():
     cfg, x, d_out, _ = make("gqa16_192", seed=2)
     out, lse = abi.window_forward(cfg, **x)
@@ -142,3 +158,74 @@ def test_refuses_what_is_not_dense_or_of_another_type():
         abi.window_forward(cfg, x["q"], x["k"].float(), x["v"])
     with pytest.raises(ValueError, match="one CUDA device"):
         abi.window_forward(cfg, x["q"], x["k"], x["v"].cpu())
+
+
+@pytest.mark.parametrize("dims", [(192, 128), (128, 64), (64, 64)], ids=str)
+def test_many_work_items_per_cta(dims):
+    """Several work items on every CTA, forward and backward, some of them partial; twenty repetitions
+    give the same bits (a hand-over between warps that is not waited for would show)."""
+    dqk, dv = dims
+    B, T, Hq, Hkv, W, ns = 2, 1210, 32, 8, 300, 70
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, d_out = r(B, T, Hq, dqk), r(B, Hkv, T, dqk), r(B, Hkv, T, dv), r(B, T, Hq, dv)
+    cfg = abi.window_config(B, T, T, Hq, Hkv, dqk, dv, W, ns)
+    first = None
+    for _ in range(20):
+        out, lse = abi.window_forward(cfg, q, k, v)
+        got = (out, lse) + abi.window_backward(cfg, q, k, v, out, lse, d_out)
+        if first is None:
+            first = got
+        for a, b in zip(first, got):
+            assert torch.equal(a, b)
+    assert abi.nsa_get_device_status() == 0
+    for b in range(B):
+        ref = window_ref(q[b:b + 1], k[b:b + 1], v[b:b + 1], visible(T, T, 0, W, ns, "cuda"), cfg.scale,
+                         d_out[b:b + 1])
+        for n, x in zip(("out", "lse", "dq", "dk", "dv"), first):
+            check(x[b:b + 1], ref[n], f"sequence {b} {n}")
+
+
+def test_turned_steps_of_a_long_batch():
+    """More query rows than the backward's natural order is kept for (64 MB of q and d_out), checked on
+    the last of several sequences; key tiles with and without sinks, whole and cut."""
+    B, T, Hq, Hkv, d, W, ns = 40, 900, 8, 1, 128, 200, 10
+    g = torch.Generator(device="cuda")
+    g.manual_seed(10)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, d_out = r(B, T, Hq, d), r(B, Hkv, T, d), r(B, Hkv, T, d), r(B, T, Hq, d)
+    assert B * T * Hq * 2 * d * 2 > 64 << 20
+    cfg = abi.window_config(B, T, T, Hq, Hkv, d, d, W, ns)
+    out, lse = abi.window_forward(cfg, q, k, v)
+    grads = abi.window_backward(cfg, q, k, v, out, lse, d_out)
+    for b in (0, B - 1):
+        one = slice(b, b + 1)
+        ref = window_ref(q[one], k[one], v[one], visible(T, T, 0, W, ns, "cuda"), cfg.scale, d_out[one])
+        for n, x in zip(("out", "lse", "dq", "dk", "dv"), (out, lse) + grads):
+            check(x[one], ref[n], f"sequence {b} {n}")
+
+
+def test_offsets_past_32_bits():
+    """Two planes of 9 million keys: the last tokens' keys lie past 2^31 elements."""
+    Tk, Tq, d, W, ns = 9_000_000, 40, 128, 70, 3
+    k = torch.zeros(1, 2, Tk, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    far = Tk - 200
+    for x in (k, v):
+        x[:, :, :ns], x[:, :, far:] = r(1, 2, ns, d), r(1, 2, 200, d)
+    assert k.numel() > 1 << 31
+    q, d_out = r(1, Tq, 4, d), r(1, Tq, 4, d)
+    cfg = abi.window_config(1, Tq, Tk, 4, 2, d, d, W, ns, Tk - Tq)
+    out, lse = abi.window_forward(cfg, q, k, v)
+    dq, dk, dv = abi.window_backward(cfg, q, k, v, out, lse, d_out)
+    near = lambda x: torch.cat([x[:, :, :ns], x[:, :, far:]], 2)  # noqa: E731
+    vis = torch.cat([torch.ones(Tq, ns, dtype=torch.bool, device="cuda"),
+                     visible(Tq, 200, 200 - Tq, W, 0, "cuda")], 1)
+    ref = window_ref(q, near(k), near(v), vis, cfg.scale, d_out)
+    for n, x in [("out", out), ("lse", lse), ("dq", dq), ("dk", near(dk)), ("dv", near(dv))]:
+        check(x, ref[n], n)
+    assert not dk[:, :, ns:far].any() and not dv[:, :, ns:far].any()

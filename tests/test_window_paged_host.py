@@ -39,7 +39,7 @@ def test_struct_layouts_match_the_header(abi):
 
 WIN_BAD = [dict(batch=0), dict(seqlen_q=-1), dict(seqlen_kv=0), dict(q_pos0=-1), dict(q_pos0=33), dict(h_q=7),
            dict(h_q=0), dict(h_kv=0), dict(d_qk=0), dict(d_v=-1), dict(window=0), dict(window=-5), dict(sink=-1),
-           dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf"))]
+           dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e-31), dict(scale=1e31)]
 WIN_OFF = [dict(d_qk=96), dict(d_qk=320), dict(d_v=192), dict(d_v=32),
            dict(seqlen_q=1, seqlen_kv=2 ** 31 - 1, q_pos0=0), dict(batch=1 << 20, seqlen_q=1 << 12, seqlen_kv=1 << 12,
                                                                    q_pos0=0)]
