@@ -60,7 +60,8 @@ nsa_status nsa_window_attn_fwd(const nsa_window_config* cfg, const void* q, cons
     WinShape s;
     nsa_status st = make_win_shape(cfg, &s);
     if (st != NSA_OK) return st;
-    if (!q || !k || !v || !out) return NSA_ERR_INVALID_ARG;
+    if (s.Tq > 0 && (!q || !out)) return NSA_ERR_INVALID_ARG;     // (buffers of zero elements may be NULL)
+    if (!k || !v) return NSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse))
         return NSA_ERR_INVALID_ARG;
     if (s.Tq == 0) return NSA_OK;
@@ -88,7 +89,8 @@ nsa_status nsa_window_attn_bwd(const nsa_window_config* cfg, const void* q, cons
     WinShape s;
     nsa_status st = make_win_shape(cfg, &s);
     if (st != NSA_OK) return st;
-    if (!q || !k || !v || !out || !lse || !d_out || !dq || !dk || !dv) return NSA_ERR_INVALID_ARG;
+    if (s.Tq > 0 && (!q || !out || !lse || !d_out || !dq)) return NSA_ERR_INVALID_ARG;
+    if (!k || !v || !dk || !dv) return NSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(lse) ||
         !aligned16(d_out) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
         return NSA_ERR_INVALID_ARG;

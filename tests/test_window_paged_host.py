@@ -79,6 +79,14 @@ def test_window_pointers(abi, bad):
     assert _status(abi, lambda: abi.nsa_window_attn_bwd(cfg, *[P] * 9, None, ws)) == "NSA_ERR_WORKSPACE"
 
 
+def test_zero_queries_need_no_query_buffers(abi):
+    cfg = _win(abi, seqlen_q=0)
+    abi.nsa_window_attn_fwd(cfg, None, P, P, None)
+    assert _status(abi, lambda: abi.nsa_window_attn_fwd(cfg, None, None, P, None)) == "NSA_ERR_INVALID_ARG"
+    assert _status(abi, lambda: abi.nsa_window_attn_bwd(cfg, None, P, P, None, None, None, None, None, P)) \
+        == "NSA_ERR_INVALID_ARG"
+
+
 PAGED_BAD = [dict(batch=0), dict(seqlen_q=0), dict(n_pages=0), dict(max_pages=0), dict(h_q=7), dict(h_kv=0),
              dict(d_qk=0), dict(d_v=0), dict(page_size=0), dict(window=-1), dict(sink=-1), dict(scale=0.0),
              dict(scale=float("nan"))]
