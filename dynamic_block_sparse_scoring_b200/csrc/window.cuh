@@ -13,11 +13,6 @@ struct WinShape {
     float scale;
 };
 
-// Key u is visible to the query at position t.
-__host__ __device__ __forceinline__ bool win_visible(const WinShape& s, int t, int u) {
-    return u <= t && (u > t - s.win || u < s.ns);
-}
-
 // Any shape: FFMA, one warp per row (window_rowwise.cu).  delta [B, Tq, Hq].
 cudaError_t launch_window_rowwise_fwd(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                       const __nv_bfloat16* v, __nv_bfloat16* out, float* lse, cudaStream_t st);

@@ -25,7 +25,12 @@
 // TMEM: S0, S1 (128 columns each, P over them as bf16), O0, O1 (d_v each).
 // Shared memory at d 192/128: Q 2 x 48 KB, K 2 x 48 KB, V 32 KB.
 // Bound by the tensor cores: a pair of tiles needs 2 x 128 x 128 x (d_qk + d_v)
-// MACs per key tile at 4096 a clock, its exponentials 2 x 16384 at 16 a clock.
+// MACs per key tile at 4096 a clock, its exponentials 2 x 16384 at 16 a clock;
+// in fact by the round trip softmax -> P V, Q K^T -> softmax of each tile, in
+// which both pipes are about half busy (without any softmax 136 us of 175).
+// Measured in bursts: 2 x 8192 tokens, 16 heads, d 128, window 1000 + 16:
+// 175 us, 730 TFLOP/s; 16384 tokens, 64 heads on 4, 192/128, window 512 + 64:
+// 420 us, 905 TFLOP/s (196 and 486 us back to back under the power cap).
 #include <math.h>
 
 #include <algorithm>
@@ -261,79 +266,73 @@ __global__ void __launch_bounds__(THREADS, 1)
                            k_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::K_OFF), 16, 1024),
                            v_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::V_OFF), CHUNK, 1024);
             auto uwait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
+            // The loops stay rolled: the short code is a little faster than the unrolled one (at the
+            // two sizes of the head comment 175.6 us against 177.0 and 425 against 434).
             uint32_t ks = 0, kph = 0, vs = 0, vph = 0;      // stage and phase of the next key / value tile
             uint32_t nq = 0, np = 0;                        // bit t: parity of tile t's next Q, next P
             bool ok = true;
             for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
                 const Work k = decode_work(a, w);
-                bool first[2] = {true, true};
-                bool pv[2] = {false, false};    // P V of key tile j - 1 is still to be issued
                 int wp = 0;                     // width of key tile j - 1
+                uint32_t pv = 0;                // bit t: P V of key tile j - 1 is still to be issued
                 // Per key tile j and query tile t: one look at the barriers (a wait for those
                 // that are not there yet) and one run of MMAs, P V of j - 1 and Q K^T of j.
-                for (int j = 0; j <= k.n; ++j) {
+#pragma unroll 1
+                for (int j = 0; ok && j <= k.n; ++j) {
                     const int wj = j < k.n ? k.width(j) : 0;
                     const uint32_t idesc_w = tc::idesc_bf16_f32(BM, 0, false, false) | ((uint32_t)(wj >> 3) << 17);
                     const uint64_t kd = tc::desc_at(k_desc, ks * L::QC * CHUNK), vd = tc::desc_at(v_desc, vs * L::VC * CHUNK);
-                    const bool qk[2] = {k.needs(0, j), k.needs(1, j)};
-#pragma unroll
+                    const uint32_t qk = (k.needs(0, j) ? 1u : 0u) | (k.needs(1, j) ? 2u : 0u);
+#pragma unroll 1
                     for (int t = 0; t < 2; ++t) {
-                        const bool last_q = j == k.e[t] - 1, last_p = j == k.e[t];
-                        const bool free_v = t == 1 || !pv[1], free_k = t == 1 || !qk[1];
-                        const uint32_t acc = first[t] ? 0u : 1u;
-                        if (!pv[t] && !qk[t]) continue;
-                        const uint32_t want = (pv[t] ? 3u : 0u) | (qk[t] ? 4u : 0u);
+                        const bool p = (pv >> t) & 1, q = (qk >> t) & 1;
+                        if (!p && !q) continue;
+                        const int e = t ? k.e[1] : k.e[0], jf = (t ? k.c[1] : k.c[0]) > 0 ? 0 : (t ? k.f[1] : k.f[0]);
+                        const uint32_t want = (p ? 3u : 0u) | (q ? 4u : 0u);
                         const uint32_t got = tc::mbar_test3(&bar.p_full[t], (np >> t) & 1, &bar.v_full[vs], vph,
                                                             &bar.k_full[ks], kph);
                         if (!__all_sync(0xffffffffu, (got & want) == want)) {
-                            if (pv[t] && (!uwait(&bar.v_full[vs], vph) || !uwait(&bar.p_full[t], (np >> t) & 1))) {
+                            if (p && (!uwait(&bar.v_full[vs], vph) || !uwait(&bar.p_full[t], (np >> t) & 1))) {
                                 ok = false;
                                 break;
                             }
-                            if (qk[t] && !uwait(&bar.k_full[ks], kph)) { ok = false; break; }
+                            if (q && !uwait(&bar.k_full[ks], kph)) { ok = false; break; }
                         }
-                        if (qk[t] && first[t] && !uwait(&bar.q_full[t], (nq >> t) & 1)) { ok = false; break; }
+                        if (q && j == jf && !uwait(&bar.q_full[t], (nq >> t) & 1)) { ok = false; break; }
                         tc::fence_after_sync();
+                        const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * DV;
                         const uint64_t qd = tc::desc_at(q_desc, t * L::QC * CHUNK);
                         if (tc::elect_one()) {
-                            if (pv[t]) {
-                                if (wp == BN) {
-#pragma unroll
-                                    for (int kk = 0; kk < BN / 16; ++kk)
-                                        tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
-                                                   tc::desc_at(vd, kk * 2048), idesc_pv, kk > 0 ? 1u : acc);
-                                } else {
-                                    for (int kk = 0; kk * 16 < wp; ++kk)
-                                        tc::mma_ts(tmem + 256 + t * DV, tmem + t * 128 + kk * 8,
-                                                   tc::desc_at(vd, kk * 2048), idesc_pv, kk > 0 ? 1u : acc);
+                            if (p) {
+                                uint32_t acc = j - 1 != jf;
+#pragma unroll 1
+                                for (int kk = 0; kk * 16 < wp; kk += 2) {       // (widths are multiples of 32)
+                                    tc::mma_ts(tO, tS + kk * 8, tc::desc_at(vd, kk * 2048), idesc_pv, acc);
+                                    tc::mma_ts(tO, tS + kk * 8 + 8, tc::desc_at(vd, kk * 2048 + 2048), idesc_pv, 1);
+                                    acc = 1;
                                 }
-                                if (free_v) tc::mma_commit(&bar.v_empty[vs]);
-                                if (last_p) tc::mma_commit(&bar.o_full[t]);
+                                if (t == 1 || !(pv & 2)) tc::mma_commit(&bar.v_empty[vs]);
+                                if (j == e) tc::mma_commit(&bar.o_full[t]);
                             }
-                            if (qk[t]) {
+                            if (q) {
+#pragma unroll 1
+                                for (int c = 0; c < L::QC; ++c)
 #pragma unroll
-                                for (int kk = 0; kk < DQK / 16; ++kk) {
-                                    const uint32_t off = (kk >> 2) * CHUNK + (kk & 3) * 32;
-                                    tc::mma_ss(tmem + t * 128, tc::desc_at(qd, off), tc::desc_at(kd, off), idesc_w,
-                                               kk > 0);
-                                }
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        tc::mma_ss(tS, tc::desc_at(qd, c * CHUNK + kk * 32), tc::desc_at(kd, c * CHUNK + kk * 32),
+                                                   idesc_w, kk > 0 || c > 0);
                                 tc::mma_commit(&bar.s_full[t]);
-                                if (free_k) tc::mma_commit(&bar.k_empty[ks]);
-                                if (last_q) tc::mma_commit(&bar.q_empty[t]);
+                                if (t == 1 || !(qk & 2)) tc::mma_commit(&bar.k_empty[ks]);
+                                if (j == e - 1) tc::mma_commit(&bar.q_empty[t]);
                             }
                         }
                         __syncwarp();
-                        if (pv[t]) {
-                            np ^= 1u << t;
-                            first[t] = false;
-                        }
-                        if (last_q) nq ^= 1u << t;
+                        if (p) np ^= 1u << t;
+                        if (j == e - 1) nq ^= 1u << t;
                     }
-                    if (!ok) break;
                     if (j > 0 && ++vs == L::VS) vs = 0, vph ^= 1;
                     if (j < k.n && ++ks == L::KS) ks = 0, kph ^= 1;
-                    pv[0] = qk[0];
-                    pv[1] = qk[1];
+                    pv = qk;
                     wp = wj;
                 }
             }
@@ -501,7 +500,9 @@ cudaError_t launch_impl(const WinShape& s, const __nv_bfloat16* q, const __nv_bf
     cudaError_t e = sm_count(&nsm, &dev);
     if (e != cudaSuccess) return e;
     const long long planes = (long long)s.B * s.Hkv;
-    // pairs of query tiles unless that would leave SMs without work
+    // pairs of query tiles unless that would leave SMs without work: a pair's chains overlap
+    // (singles 280 us against 175, 710 against 420), 32 query tiles finish earlier on 32 SMs
+    // (1000 tokens, 4 heads on 1, d 64: 8.1 us against 9.6)
     a.nt = (a.n_tt + 1) / 2 * planes >= nsm ? 2 : 1;
     a.n_work = (int)((a.n_tt + a.nt - 1) / a.nt * planes);
     CUtensorMap mq, mk, mv;
@@ -518,6 +519,9 @@ cudaError_t launch_impl(const WinShape& s, const __nv_bfloat16* q, const __nv_bf
 
 }  // namespace
 
+// What fits TMEM (512 columns) and shared memory, and a token's heads in half a query tile.
+// Everything else runs on FFMA, 100 times slower where both serve (16384 tokens, 64 heads
+// on 4, 192/128, window 512 + 64: 68.4 ms against 0.42).
 bool window_tc_supported(const WinShape& s) {
     return s.dqk <= 192 && s.dv <= 128 && s.G <= 64;
 }
