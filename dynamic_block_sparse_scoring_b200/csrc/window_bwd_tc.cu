@@ -432,9 +432,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::mbar_wait_bounded(&bar.drain, 0, WAIT_NS);
         } else if (MODE == DQ && warp >= 2) {
             // ------------------------------------------------ (lse, delta) of a query tile's rows
-            // LPR lanes hold a row's d_v values, 16 bytes each; warps 2 and 3 take half of the rows
-            constexpr int LPR = DV / 8, RPI = 32 / LPR, U = 4;
-            const int half = (warp - 2) * (BM / 2), sub = lane / LPR, col = (lane % LPR) * 8;
+            // LPR lanes hold a row's d_v values, 16 bytes each; warps 2 and 3 take half of the
+            // rows, U x RPI of them in flight at a time.  Their sums over the lanes are taken
+            // together: each round halves the rows that a lane carries.
+            constexpr int LPR = DV / 8, RPI = 32 / LPR, U = 4, HALF = BM / 2;
+            const int half = (warp - 2) * HALF, sub = lane / LPR, col = (lane % LPR) * 8;
             uint32_t n = 0;
             bool ok = true;
             for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round, ++n) {
@@ -442,52 +444,76 @@ __global__ void __launch_bounds__(THREADS, 1)
                 decode_work<MODE>(a, w, &k);
                 const int buf = n & 1;
                 if (!warp_wait(&bar.aux_empty[buf], ((n >> 1) & 1) ^ 1)) { ok = false; break; }
-                for (int r0 = half; r0 < half + BM / 2; r0 += RPI * U) {
+                const int toks = min(a.tok, s.Tq - k.first);
+                const long long row0 = ((long long)k.b * s.Tq + k.first) * s.Hq + k.kvh * s.G;
+                float2 ls;                          // lse of rows half + lane and half + 32 + lane
+                long long at[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = half + 32 * e + lane, tt = r / s.G;
+                    at[e] = tt < toks ? row0 + (long long)tt * s.Hq + (r - tt * s.G) : -1;
+                    (e ? ls.y : ls.x) = at[e] >= 0 ? a.lse[at[e]] : INFINITY;
+                }
+                int tt = (half + sub) / s.G, h = half + sub - tt * s.G;
+                float2* dst = aux + buf * BM + half;
+#pragma unroll 1
+                for (int r0 = 0; r0 < HALF; r0 += RPI * U) {
                     uint4 x[U], y[U];
-                    float ls[U];
-                    long long row[U];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        const int r = r0 + u * RPI + sub, tt = r / s.G, i = k.first + tt;
-                        row[u] = tt < a.tok && i < s.Tq
-                                     ? ((long long)k.b * s.Tq + i) * s.Hq + k.kvh * s.G + (r - tt * s.G)
-                                     : -1;
                         x[u] = y[u] = make_uint4(0, 0, 0, 0);
-                        ls[u] = INFINITY;
-                        if (row[u] >= 0) {
-                            x[u] = *reinterpret_cast<const uint4*>(a.out + row[u] * DV + col);
-                            y[u] = *reinterpret_cast<const uint4*>(a.d_out + row[u] * DV + col);
-                            ls[u] = a.lse[row[u]];
+                        if (tt < toks) {
+                            const size_t o = (size_t)(row0 + (long long)tt * s.Hq + h) * DV + col;
+                            x[u] = *reinterpret_cast<const uint4*>(a.out + o);
+                            y[u] = *reinterpret_cast<const uint4*>(a.d_out + o);
                         }
+                        for (h += RPI; h >= s.G; h -= s.G) ++tt;
                     }
+                    float d[U];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        float f[8], h[8], d = 0.f;
+                        float f[8], g[8];
                         unpack8(x[u], f);
-                        unpack8(y[u], h);
+                        unpack8(y[u], g);
+                        d[u] = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) d = fmaf(f[e], h[e], d);
+                        for (int e = 0; e < 8; ++e) d[u] = fmaf(f[e], g[e], d[u]);
+                    }
+                    // after the rounds lane bits LPR / 2 and LPR / 4 name the row u
+                    int u0 = 0;
 #pragma unroll
-                        for (int o = LPR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                        if (lane % LPR == 0) {
-                            aux[buf * BM + r0 + u * RPI + sub] = make_float2(ls[u] * LOG2E, d);
-                            if (row[u] >= 0) a.delta[row[u]] = d;
+                    for (int c = U / 2, o = LPR / 2; c > 0; c >>= 1, o >>= 1) {
+                        const bool up = lane & o;
+                        u0 += up ? c : 0;
+#pragma unroll
+                        for (int u = 0; u < c; ++u) {
+                            const float send = up ? d[u] : d[u + c];
+                            d[u] = (up ? d[u + c] : d[u]) + __shfl_xor_sync(0xffffffffu, send, o);
                         }
                     }
+#pragma unroll
+                    for (int o = LPR / 2 / U; o > 0; o >>= 1) d[0] += __shfl_xor_sync(0xffffffffu, d[0], o);
+                    if ((lane & (LPR / U - 1)) == 0) dst[r0 + u0 * RPI + sub].y = d[0];
+                }
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float2* v = dst + 32 * e + lane;
+                    v->x = (e ? ls.y : ls.x) * LOG2E;
+                    if (at[e] >= 0) a.delta[at[e]] = v->y;
                 }
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bar.aux_full[buf]);
             }
             if (!ok) give_up();
-        } else if (MODE == DKV && warp == 2) {
+        } else if (MODE == DKV && warp >= 2) {
             // ------------------------------------------------ (lse, delta) of a step's rows
             // As 16 more columns of the products: -lse / scale and -delta, each the sum of
             // three bf16 (24 bits), against the residents' (1, 1, 1, 0, ..).  S and D then come
             // as q.k - lse / scale and do.v - delta, and the threads, whose columns the
-            // queries are, need no other value of theirs.
+            // queries are, need no other value of theirs.  Warps 2 and 3 take the steps in
+            // turn; the values of a warp's next step are on their way while it writes this one's.
             pdl_wait();                             // delta
-            uint32_t g = 0;
-            bool ok = true;
             const float inv_scale = 1.f / s.scale;
             auto three = [](float v) {
                 const __nv_bfloat16 h = __float2bfloat16_rn(v);
@@ -495,35 +521,63 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const __nv_bfloat16 m = __float2bfloat16_rn(r1);
                 return make_uint4(tc::pack_bf16x2(bf2f(h), bf2f(m)), tc::pack_bf16x2(r1 - bf2f(m), 0.f), 0, 0);
             };
-            for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
-                Work k;
-                if (!decode_work<MODE>(a, w, &k) || k.n == 0) continue;
-                for (int i = 0; i < k.n; ++i, ++g) {
-                    const int st = g % L::NST;
-                    float2 v[2];
+            int tt[2], head[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = lane + 32 * e, tt = r / s.G, tok = k.token(i, a.tok) + tt;
-                        v[e] = make_float2(-3e38f, 0.f);        // p = 0: no query
-                        if (tt < a.tok && tok < s.Tq) {
-                            const size_t row = ((size_t)k.b * s.Tq + tok) * s.Hq + k.kvh * s.G + (r - tt * s.G);
-                            v[e] = make_float2(-a.lse[row] * inv_scale, -a.delta[row]);
-                        }
-                    }
-                    if (!warp_wait(&bar.t_empty[st], ((g / L::NST) & 1) ^ 1)) { ok = false; break; }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = lane + 32 * e, half = (r >> 2) & 1;
-                        uint4* x = reinterpret_cast<uint4*>(sm + L::AUX_OFF + L::EXT_A + st * 2 * L::EXT_B + r * 32);
-                        x[half] = three(v[e].x);
-                        x[half ^ 1] = make_uint4(0, 0, 0, 0);
-                        x[L::EXT_B / 16 + half] = three(v[e].y);
-                        x[L::EXT_B / 16 + (half ^ 1)] = make_uint4(0, 0, 0, 0);
-                    }
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar.t_full[st]);
+            for (int e = 0; e < 2; ++e) {
+                tt[e] = (lane + 32 * e) / s.G;
+                head[e] = lane + 32 * e - tt[e] * s.G;
+            }
+            Work k;
+            int round = -1, i = 0;
+            uint32_t g = 0;                         // step i of work k, of all steps
+            // the next step of an odd (warp 3) or even number; false: there is none
+            auto advance = [&](int by) {
+                i += by;
+                g += by;
+                while (round < 0 || i >= k.n) {
+                    if (round >= 0) i -= k.n;
+                    const int w = dealt(++round);
+                    if (w >= a.n_work) return false;
+                    if (!decode_work<MODE>(a, w, &k)) k.n = 0;
                 }
+                return true;
+            };
+            auto load = [&](float2* v) {
+                const int first = k.token(i, a.tok);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    v[e] = make_float2(3e38f, 0.f);             // p = 0: no query
+                    if (tt[e] < a.tok && first + tt[e] < s.Tq) {
+                        const size_t row = ((size_t)k.b * s.Tq + first + tt[e]) * s.Hq + k.kvh * s.G + head[e];
+                        v[e] = make_float2(a.lse[row], a.delta[row]);
+                    }
+                }
+            };
+            bool ok = true;
+            float2 v[2], next[2];
+            bool more = advance(warp - 2);
+            if (more) load(next);
+            while (more) {
+                const uint32_t e0 = g;
+                v[0] = next[0];
+                v[1] = next[1];
+                more = advance(2);
+                if (more) load(next);
+                const int st = e0 % L::NST;
+                if (!warp_wait(&bar.t_empty[st], ((e0 / L::NST) & 1) ^ 1)) { ok = false; break; }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = lane + 32 * e, half = (r >> 2) & 1;
+                    uint4* x = reinterpret_cast<uint4*>(sm + L::AUX_OFF + L::EXT_A + st * 2 * L::EXT_B + r * 32);
+                    // (of a row without a query: -3e38, not times 1 / scale, which could pass fp32)
+                    x[half] = three(v[e].x == 3e38f ? -3e38f : -v[e].x * inv_scale);
+                    x[half ^ 1] = make_uint4(0, 0, 0, 0);
+                    x[L::EXT_B / 16 + half] = three(-v[e].y);
+                    x[L::EXT_B / 16 + (half ^ 1)] = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.t_full[st]);
             }
             if (!ok) give_up();
         }
