@@ -81,16 +81,20 @@ struct PagedArgs {
     const int32_t* lens;
     __nv_bfloat16* out;
     float* lse;
-    long long* prefix;      // [B + 1] first tile of every sequence's units
     float* part_o;          // [2 * workers][ROWS][dv]
     float* part_lse;        // [2 * workers][ROWS]
     int RT;                 // row tiles per (sequence, KV head)
     float scale_log2;
 };
 
+// a / b for a >= 0, b > 0, by the short 32-bit division where both fit.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Tiles per worker when `total` tiles are dealt to `workers`.
-__host__ __device__ __forceinline__ long long share_of(long long total, int workers) {
-    const long long x = (total + workers - 1) / workers;
+__device__ __forceinline__ long long share_of(long long total, int workers) {
+    const long long x = quotient(total + workers - 1, workers);
     return x < MIN_TILES ? MIN_TILES : x;
 }
 
@@ -178,15 +182,6 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
     if (threadIdx.x == THREADS - 1) pre[THREADS] = inc;
     __syncthreads();
     const long long total = pre[THREADS];
-    if (blockIdx.x == 0) {                         // for the join
-        long long at = inc - mine;
-        for (int b = c0; b < c1; ++b) {
-            a.prefix[b] = at;
-            at += (long long)seq_tiles(s, paged_len(s, a.lens, b)).n * per_seq;
-        }
-        if (threadIdx.x == 0) a.prefix[s.B] = total;
-    }
-
     const int workers = gridDim.x * L::WARPS;
     const int me = warp * gridDim.x + blockIdx.x;  // neighbours on different SMs
     const long long per = share_of(total, workers);
@@ -219,8 +214,8 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
             sq = seq_tiles(s, paged_len(s, a.lens, b));
             continue;
         }
-        const int unit = (int)((g - base) / sq.n);
-        const int i0 = (int)((g - base) % sq.n);
+        const int unit = (int)quotient(g - base, sq.n);
+        const int i0 = (int)(g - base - (long long)unit * sq.n);
         const int i1 = (int)min((long long)sq.n, i0 + (g1 - g));
         const int h = unit / a.RT, rt = unit % a.RT;
         const int t_first = sq.len - s.Tq;              // position of query 0 (may be below 0)
@@ -413,7 +408,8 @@ constexpr int JOIN_WARPS = 4;
 template <int DV, bool SPLIT>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const PagedArgs a, int workers) {
     constexpr int NC = DV / 64;                     // column pairs per lane
-    __shared__ float2 acc_s[SPLIT ? JOIN_WARPS : 1][SPLIT ? DV / 2 : 1];
+    __shared__ float2 acc_s[SPLIT ? JOIN_WARPS : 1][SPLIT ? DV / 2 : 1], ml_s[JOIN_WARPS];
+    __shared__ long long pre_s[JOIN_WARPS], tot_s[JOIN_WARPS];
     const PagedShape& s = a.s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per_seq = s.Hkv * a.RT;
@@ -421,53 +417,103 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const Paged
     const int h = unit / a.RT, rt = unit % a.RT;
     const int ru = SPLIT ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;     // row of the unit
     const int r = rt * ROWS + ru;
+    // which shares the unit was cut into: from the lengths, while the shares are still computed
+    long long p0 = 0, total = 0;
+    for (int i = threadIdx.x; i < s.B; i += JOIN_WARPS * 32) {
+        const long long t = (long long)seq_tiles(s, paged_len(s, a.lens, i)).n * per_seq;
+        total += t;
+        if (i < b) p0 += t;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        p0 += __shfl_xor_sync(0xffffffffu, p0, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) {
+        pre_s[warp] = p0;
+        tot_s[warp] = total;
+    }
+    __syncthreads();
+    p0 = total = 0;
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) {
+        p0 += pre_s[w];
+        total += tot_s[w];
+    }
+    const int n = seq_tiles(s, paged_len(s, a.lens, b)).n;
+    const long long per = share_of(total, workers);
+    const long long first = p0 + (long long)unit * n, last = first + n - 1;
+    const int w0 = (int)quotient(first, per), w1 = n > 0 ? (int)quotient(last, per) : w0 - 1;
     pdl_wait();
     if (r >= s.Tq * s.G) return;                    // (whole CTAs when SPLIT)
-    const size_t orow = ((size_t)b * s.Tq + r / s.G) * s.Hq + h * s.G + r % s.G;
-    const long long p0 = a.prefix[b], n = (a.prefix[b + 1] - p0) / per_seq;
-    const long long per = share_of(a.prefix[s.B], workers);
-    const long long first = p0 + unit * n, last = first + n - 1;
-    const int w0 = (int)(first / per), w1 = n > 0 ? (int)(last / per) : w0 - 1;
     if (n > 0 && w0 == w1) return;                  // finished by its worker
+    const size_t orow = ((size_t)b * s.Tq + r / s.G) * s.Hq + h * s.G + r % s.G;
     auto part_row = [&](int w) {                    // only w0 starts the unit
         return (size_t)(2 * w + (w == w0 ? 1 : 0)) * ROWS + ru;
     };
-    float mx = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 32) mx = fmaxf(mx, a.part_lse[part_row(w)]);
-    mx = warp_max(mx);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
+    // lane's columns of the shares so far: acc and sum under the running maximum mx
+    float mx = -INFINITY, sum = 0.f;
     float2 acc[NC];
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[c] = make_float2(0.f, 0.f);
-    for (int w = w0 + lane; w <= w1; w += 32) sum += tc::ex2(a.part_lse[part_row(w)] - ref);
-    sum = warp_sum(sum);
-#pragma unroll 8
-    for (int w = w0 + (SPLIT ? warp : 0); w <= w1; w += SPLIT ? JOIN_WARPS : 1) {
-        const size_t pr = part_row(w);
-        const float wt = tc::ex2(a.part_lse[pr] - ref);
+    constexpr int U = 8, STEP = SPLIT ? JOIN_WARPS : 1;
+    for (int w = w0 + (SPLIT ? warp : 0); w <= w1; w += U * STEP) {
+        float ls[U];
+        float2 x[U][NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const float2 x = reinterpret_cast<const float2*>(a.part_o + pr * DV)[c * 32 + lane];
-            acc[c] = make_float2(fmaf(wt, x.x, acc[c].x), fmaf(wt, x.y, acc[c].y));
+        for (int u = 0; u < U; ++u) {
+            const bool ok = w + u * STEP <= w1;
+            const size_t pr = part_row(ok ? w + u * STEP : w);
+            ls[u] = ok ? a.part_lse[pr] : -INFINITY;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                x[u][c] = ok ? reinterpret_cast<const float2*>(a.part_o + pr * DV)[c * 32 + lane] : make_float2(0.f, 0.f);
+        }
+        float top = mx;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, ls[u]);
+        const float ref = top == -INFINITY ? 0.f : top, old = tc::ex2(mx - ref);
+        mx = top;
+        sum *= old;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[c] = make_float2(acc[c].x * old, acc[c].y * old);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float wt = tc::ex2(ls[u] - ref);
+            sum += wt;
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+                acc[c] = make_float2(fmaf(wt, x[u][c].x, acc[c].x), fmaf(wt, x[u][c].y, acc[c].y));
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * DV);
     if (SPLIT) {
+        if (lane == 0) ml_s[warp] = make_float2(mx, sum);
 #pragma unroll
         for (int c = 0; c < NC; ++c) acc_s[warp][c * 32 + lane] = acc[c];
         __syncthreads();
+        float wt[JOIN_WARPS];
+        mx = -INFINITY;
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) mx = fmaxf(mx, ml_s[w].x);
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) {
+            wt[w] = mx == -INFINITY ? 0.f : tc::ex2(ml_s[w].x - mx);
+            sum = fmaf(wt[w], ml_s[w].y, sum);
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
         for (int c = threadIdx.x; c < DV / 2; c += JOIN_WARPS * 32) {
             float x = 0.f, y = 0.f;
 #pragma unroll
             for (int w = 0; w < JOIN_WARPS; ++w) {
-                x += acc_s[w][c].x;
-                y += acc_s[w][c].y;
+                x = fmaf(wt[w], acc_s[w][c].x, x);
+                y = fmaf(wt[w], acc_s[w][c].y, y);
             }
             dst[c] = tc::pack_bf16x2(x * inv, y * inv);
         }
     } else {
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) dst[c * 32 + lane] = tc::pack_bf16x2(acc[c].x * inv, acc[c].y * inv);
     }
@@ -502,8 +548,7 @@ cudaError_t launch_impl(PagedArgs a, int n_units, int rows, cudaStream_t st) {
 }  // namespace
 
 size_t paged_attn_ws_bytes(const PagedShape& s) {
-    return up256((size_t)(s.B + 1) * 8) + up256((size_t)2 * MAX_WORKERS * ROWS * s.dv * 4) +
-           up256((size_t)2 * MAX_WORKERS * ROWS * 4);
+    return up256((size_t)2 * MAX_WORKERS * ROWS * s.dv * 4) + up256((size_t)2 * MAX_WORKERS * ROWS * 4);
 }
 
 cudaError_t launch_paged_attn(const PagedShape& s, const __nv_bfloat16* q, const __nv_bfloat16* kp,
@@ -518,8 +563,6 @@ cudaError_t launch_paged_attn(const PagedShape& s, const __nv_bfloat16* q, const
     a.lens = lens;
     a.out = out;
     a.lse = lse;
-    a.prefix = reinterpret_cast<long long*>(ws);
-    ws += up256((size_t)(s.B + 1) * 8);
     a.part_o = reinterpret_cast<float*>(ws);
     ws += up256((size_t)2 * MAX_WORKERS * ROWS * s.dv * 4);
     a.part_lse = reinterpret_cast<float*>(ws);
