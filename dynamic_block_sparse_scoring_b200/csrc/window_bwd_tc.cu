@@ -193,6 +193,76 @@ __device__ __forceinline__ uint32_t range_bits(int lo, int hi, int w) {
     return (0xFFFFFFFFu >> (31 - b)) & (0xFFFFFFFFu << a);
 }
 
+// DQ: (lse log2 e, delta) of N rows of a query tile, from row r0 on, by one warp: into dst and,
+// delta, into global memory.  LPR lanes hold a row's d_v values, 16 bytes each, U x RPI rows
+// are in flight at a time.  Their sums over the lanes are taken together: each round halves
+// the rows that a lane carries.
+template <int DV, int N, int U>
+__device__ __forceinline__ void rows_delta(const Args& a, const Work& k, int r0, int lane, float2* dst) {
+    constexpr int LPR = DV / 8, RPI = 32 / LPR, E = (N + 31) / 32;
+    static_assert(N % (RPI * U) == 0 && U <= LPR, "rows per step");
+    const WinShape& s = a.s;
+    const int sub = lane / LPR, col = (lane % LPR) * 8;
+    const int toks = min(a.tok, s.Tq - k.first);
+    const long long row0 = ((long long)k.b * s.Tq + k.first) * s.Hq + k.kvh * s.G;
+    float ls[E];                                    // lse of rows r0 + 32 e + lane
+    long long at[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int r = r0 + 32 * e + lane, tt = r / s.G;
+        at[e] = tt < toks && 32 * e + lane < N ? row0 + (long long)tt * s.Hq + (r - tt * s.G) : -1;
+        ls[e] = at[e] >= 0 ? a.lse[at[e]] : INFINITY;
+    }
+    int tt = (r0 + sub) / s.G, h = r0 + sub - tt * s.G;
+#pragma unroll 1
+    for (int i = 0; i < N; i += RPI * U) {
+        uint4 x[U], y[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x[u] = y[u] = make_uint4(0, 0, 0, 0);
+            if (tt < toks) {
+                const size_t o = (size_t)(row0 + (long long)tt * s.Hq + h) * DV + col;
+                x[u] = *reinterpret_cast<const uint4*>(a.out + o);
+                y[u] = *reinterpret_cast<const uint4*>(a.d_out + o);
+            }
+            for (h += RPI; h >= s.G; h -= s.G) ++tt;
+        }
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float f[8], g[8];
+            unpack8(x[u], f);
+            unpack8(y[u], g);
+            d[u] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[u] = fmaf(f[e], g[e], d[u]);
+        }
+        // after the rounds the high bits of the lane within its row name the row u
+        int u0 = 0;
+#pragma unroll
+        for (int c = U / 2, o = LPR / 2; c > 0; c >>= 1, o >>= 1) {
+            const bool up = lane & o;
+            u0 += up ? c : 0;
+#pragma unroll
+            for (int u = 0; u < c; ++u) {
+                const float send = up ? d[u] : d[u + c];
+                d[u] = (up ? d[u + c] : d[u]) + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        }
+#pragma unroll
+        for (int o = LPR / 2 / U; o > 0; o >>= 1) d[0] += __shfl_xor_sync(0xffffffffu, d[0], o);
+        if ((lane & (LPR / U - 1)) == 0) dst[i + u0 * RPI + sub].y = d[0];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (32 * e + lane >= N) continue;
+        float2* v = dst + 32 * e + lane;
+        v->x = ls[e] * LOG2E;
+        if (at[e] >= 0) a.delta[at[e]] = v->y;
+    }
+}
+
 template <int DQK, int DV, int MODE>
 __global__ void __launch_bounds__(THREADS, 1)
     window_bwd_tc_kernel(const __grid_constant__ CUtensorMap map_r1, const __grid_constant__ CUtensorMap map_r2,
@@ -432,75 +502,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::mbar_wait_bounded(&bar.drain, 0, WAIT_NS);
         } else if (MODE == DQ && warp >= 2) {
             // ------------------------------------------------ (lse, delta) of a query tile's rows
-            // LPR lanes hold a row's d_v values, 16 bytes each; warps 2 and 3 take half of the
-            // rows, U x RPI of them in flight at a time.  Their sums over the lanes are taken
-            // together: each round halves the rows that a lane carries.
-            constexpr int LPR = DV / 8, RPI = 32 / LPR, U = 4, HALF = BM / 2;
-            const int half = (warp - 2) * HALF, sub = lane / LPR, col = (lane % LPR) * 8;
+            // warps 2 and 3 take half of the rows, a tile ahead; the first tile's are the softmax warps'
             uint32_t n = 0;
             bool ok = true;
             for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round, ++n) {
-                Work k;
-                decode_work<MODE>(a, w, &k);
-                const int buf = n & 1;
+                const int buf = n & 1, half = (warp - 2) * (BM / 2);
                 if (!warp_wait(&bar.aux_empty[buf], ((n >> 1) & 1) ^ 1)) { ok = false; break; }
-                const int toks = min(a.tok, s.Tq - k.first);
-                const long long row0 = ((long long)k.b * s.Tq + k.first) * s.Hq + k.kvh * s.G;
-                float2 ls;                          // lse of rows half + lane and half + 32 + lane
-                long long at[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = half + 32 * e + lane, tt = r / s.G;
-                    at[e] = tt < toks ? row0 + (long long)tt * s.Hq + (r - tt * s.G) : -1;
-                    (e ? ls.y : ls.x) = at[e] >= 0 ? a.lse[at[e]] : INFINITY;
-                }
-                int tt = (half + sub) / s.G, h = half + sub - tt * s.G;
-                float2* dst = aux + buf * BM + half;
-#pragma unroll 1
-                for (int r0 = 0; r0 < HALF; r0 += RPI * U) {
-                    uint4 x[U], y[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        x[u] = y[u] = make_uint4(0, 0, 0, 0);
-                        if (tt < toks) {
-                            const size_t o = (size_t)(row0 + (long long)tt * s.Hq + h) * DV + col;
-                            x[u] = *reinterpret_cast<const uint4*>(a.out + o);
-                            y[u] = *reinterpret_cast<const uint4*>(a.d_out + o);
-                        }
-                        for (h += RPI; h >= s.G; h -= s.G) ++tt;
-                    }
-                    float d[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        float f[8], g[8];
-                        unpack8(x[u], f);
-                        unpack8(y[u], g);
-                        d[u] = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) d[u] = fmaf(f[e], g[e], d[u]);
-                    }
-                    // after the rounds lane bits LPR / 2 and LPR / 4 name the row u
-                    int u0 = 0;
-#pragma unroll
-                    for (int c = U / 2, o = LPR / 2; c > 0; c >>= 1, o >>= 1) {
-                        const bool up = lane & o;
-                        u0 += up ? c : 0;
-#pragma unroll
-                        for (int u = 0; u < c; ++u) {
-                            const float send = up ? d[u] : d[u + c];
-                            d[u] = (up ? d[u + c] : d[u]) + __shfl_xor_sync(0xffffffffu, send, o);
-                        }
-                    }
-#pragma unroll
-                    for (int o = LPR / 2 / U; o > 0; o >>= 1) d[0] += __shfl_xor_sync(0xffffffffu, d[0], o);
-                    if ((lane & (LPR / U - 1)) == 0) dst[r0 + u0 * RPI + sub].y = d[0];
-                }
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float2* v = dst + 32 * e + lane;
-                    v->x = (e ? ls.y : ls.x) * LOG2E;
-                    if (at[e] >= 0) a.delta[at[e]] = v->y;
+                if (n > 0) {
+                    Work k;
+                    decode_work<MODE>(a, w, &k);
+                    rows_delta<DV, BM / 2, 4>(a, k, half, lane, aux + buf * BM + half);
                 }
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bar.aux_full[buf]);
@@ -604,6 +615,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int pos = MODE == DQ ? s.q0 + k.first + tt : k.first + r;     // query position or key
             if (MODE == DQ) {
                 const int buf = n & 1;
+                if (n == 0) {                       // with eight warps: 16 rows each, in one step
+                    constexpr int SHARE = BM / 8;
+                    rows_delta<DV, SHARE, SHARE * DV / 256>(a, k, (warp - 4) * SHARE, lane, aux + (warp - 4) * SHARE);
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                }
                 if (!warp_wait(&bar.aux_full[buf], (n >> 1) & 1)) { ok = false; break; }
                 mine = aux[buf * BM + r];
                 __syncwarp();
