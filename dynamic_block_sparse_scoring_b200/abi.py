@@ -459,7 +459,7 @@ def window_forward(cfg: NsaWindowConfig, q, k, v):
     B, Tq, Hq, Hkv, Tk, d, dv = (cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.h_kv, cfg.seqlen_kv, cfg.d_qk, cfg.d_v)
     dev = _device(("q", q, (B, Tq, Hq, d), _BF16), ("k", k, (B, Hkv, Tk, d), _BF16),
                   ("v", v, (B, Hkv, Tk, dv), _BF16))
-    out = q.new_empty((B, Tq, Hq, dv))
+    out = torch.empty_like(q) if dv == d else q.new_empty((B, Tq, Hq, dv))
     lse = q.new_empty((B, Tq, Hq), dtype=_F32)
     _run(lib.nsa_window_attn_fwd, dev, cfg, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
          lse.data_ptr())
@@ -499,7 +499,7 @@ def paged_attention(cfg: NsaPagedConfig, q, k_pages, v_pages, table, lens):
     dev = _device(("q", q, (B, Tq, Hq, cfg.d_qk), _BF16), *_cache(cfg, k_pages, v_pages),
                   *_books(cfg, table, lens))
     n = _size(lib.nsa_paged_workspace_size, cfg)
-    out = q.new_empty((B, Tq, Hq, cfg.d_v))
+    out = torch.empty_like(q) if cfg.d_v == cfg.d_qk else q.new_empty((B, Tq, Hq, cfg.d_v))
     lse = q.new_empty((B, Tq, Hq), dtype=_F32)
     ws = q.new_empty(n, dtype=_U8)
     _run(lib.nsa_paged_attn_fwd, dev, cfg, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),

@@ -822,8 +822,8 @@ Split make_split(const WinShape& s) {
     const int half = (int)std::min<long long>(std::max<long long>((total / SMS + 1) / 2, MIN_CHUNK), INT32_MAX);
     p.chunk_s = std::max(1, std::min(half, n_s));
     p.chunk_o = std::max(1, planes * others >= 2 * SMS ? n_o : std::min(half, n_o));
-    p.sp_s = ceil_div(n_s, p.chunk_s);
-    p.sp_o = ceil_div(n_o, p.chunk_o);
+    p.sp_s = p.nsk > 0 ? ceil_div(n_s, p.chunk_s) : 1;
+    p.sp_o = others > 0 ? ceil_div(n_o, p.chunk_o) : 1;
     p.slots_s = p.sp_s > 1 ? (int)(planes * p.nsk * p.sp_s) : 0;
     return p;
 }

@@ -84,6 +84,24 @@ def test_other_scales(scale):
         check(got, ref[n], n)
 
 
+@pytest.mark.parametrize("group", [1, 5, 33])
+@pytest.mark.parametrize("window", [1, 3, 90])
+def test_short_windows_without_sinks(window, group):
+    """No key tile holds sinks, and none of the others has enough queries to be cut into items."""
+    Tq, q0 = 700, 37
+    Tk = q0 + Tq
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, d_out = r(1, Tq, group, 64), r(1, 1, Tk, 64), r(1, 1, Tk, 128), r(1, Tq, group, 128)
+    cfg = abi.window_config(1, Tq, Tk, group, 1, 64, 128, window, 0, q0)
+    out, lse = abi.window_forward(cfg, q, k, v)
+    grads = abi.window_backward(cfg, q, k, v, out, lse, d_out)
+    ref = window_ref(q, k, v, visible(Tq, Tk, q0, window, 0, "cuda"), cfg.scale, d_out)
+    for n, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse) + grads):
+        check(got, ref[n], n)
+
+
 def test_lse_is_optional_and_calls_repeat_bit_for_bit():
     cfg, x, d_out, _ = make("gqa16_192", seed=2)
     out, lse = abi.window_forward(cfg, **x)
