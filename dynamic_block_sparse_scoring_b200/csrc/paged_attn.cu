@@ -20,9 +20,9 @@
 // need a few percent of the tensor cores at full HBM rate, and a warp keeps
 // its whole state in registers, without a CTA-wide hand-over per tile.
 // Bound by HBM: 64 sequences of up to 32768 keys, 64 heads on 4, 192/128:
-// 404 us, 6.5 TB/s in a burst; 48 x 4 tokens, 32 heads on 8, d 128, window
-// 4096 + 16, pages of 16: 137 us, 5.5 TB/s, the join 8 of them.  One sequence of
-// 1000 keys is two launches of dependent loads: 14 us.
+// 400 us, 6.5 TB/s in a burst; 48 x 4 tokens, 32 heads on 8, d 128, window
+// 4096 + 16, pages of 16: 136 us, 5.6 TB/s, the join 6 of them.  One sequence of
+// 1000 keys is two launches of dependent loads: 10.8 us (7.8 without the join).
 #include <math.h>
 
 #include <algorithm>
@@ -39,8 +39,8 @@ constexpr int ROWS = 16;                // query rows per unit
 // Ring stages of a worker: at 192/128 they fill shared memory with 8 workers, 208 KB in flight
 // per SM, four times what HBM's latency needs.
 constexpr int KST = 3, VST = 2;
-// Least share of a worker: 1000 keys, 16 heads, d 128 take 15.6 us at 1, 14.2 at 2, 14.8 at 4,
-// 17.4 at 8 (more to join against a longer walk).
+// Least share of a worker: 1000 keys, 16 heads, d 128 take 11.1 us at 1, 10.8 at 2, 12.9 at 4
+// (more to join against a longer walk).
 constexpr int MIN_TILES = 2;
 
 template <int DQK, int DV>
@@ -401,8 +401,9 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
 // Joins the shares of a unit's rows; units without keys get 0 and -inf.  A warp
 // has a row (blockIdx.y: four rows), or, with fewer than four rows (one query
 // head per KV head), the four warps have one row's shares w, w + 4, ...: such
-// units are few and their shares many (16 heads, one sequence of 1000 keys: the
-// join takes 9.7 us, a warp per row 16).
+// units are few and their shares many (both kernels, one sequence of 1000 keys,
+// 16 heads: 10.8 us, with a warp per row 12.2; 48 x 4 tokens with 4 heads a KV
+// head: 148 us, with a warp per row 135).
 constexpr int JOIN_WARPS = 4;
 
 template <int DV, bool SPLIT>

@@ -29,12 +29,12 @@
 // of a step the tensor cores' time of a whole step.
 // Bound by the tensor cores and shared memory: a step (64 streamed rows) is
 // 128 x 64 x (2 d_qk + d_v) MACs in DQ, (2 d_qk + 2 d_v) in DKV, at 4096 a
-// clock; S and D (N = 64, both operands in shared memory) read 6 KB for 32
-// clocks of MMA, 1.5 times what shared memory gives.
+// clock; S and D (N = 64, both operands in shared memory) take 48 clocks for 32
+// of MMA, for the 6 KB that they read, and the copies write 40 KB a step.
 // Measured in bursts, forward included: 8192 tokens, 64 heads on 4, 192/128,
-// window 512 + 64: 1080 us, 620 TFLOP/s; 4096 tokens, 16 heads, d 128, fully
-// causal: 363 us, 663 TFLOP/s (counting five products of the backward, not the
-// seven done); 1184 and 377 us back to back under the power cap.
+// window 512 + 64: 980 us, 684 TFLOP/s; 4096 tokens, 16 heads, d 128, fully
+// causal: 342 us, 703 TFLOP/s (counting five products of the backward, not the
+// seven done); 1114 and 371 us back to back under the power cap.
 #include <math.h>
 
 #include <algorithm>
@@ -57,7 +57,7 @@ constexpr int THREADS = 384;
 constexpr uint64_t WAIT_NS = 1000000000ull;
 constexpr int SMS = 148;                        // the split of key tiles is planned for this many SMs
 // Least steps of an item of a split key tile: 1000 tokens, 4 heads on 1, d 64, window 128 + 4
-// take 35.3 us at 8, 32.5 at 4, 32.4 at 2; fewer steps only mean more partial sums.
+// took 35.3 us at 8, 32.5 at 4, 32.4 at 2; fewer steps only mean more partial sums.
 constexpr int MIN_CHUNK = 4;
 constexpr float LOG2E = 1.4426950408889634f;
 
