@@ -123,7 +123,9 @@ __device__ __forceinline__ Work decode_work(const Args& a, int w) {
     k.lo = max(0, k.pf[0] - s.win + 1);
     k.sl = min(s.ns, k.lo);
     k.nst = (k.sl + BN - 1) / BN;
-    if (k.lo < k.nst * BN) k.lo = k.sl = k.nst = 0;     // they meet: one range from 0
+    // They meet, or sinks lie in the window's tiles (which the second query tile may need for
+    // these alone): one range from 0.
+    if (k.lo < k.nst * BN || s.ns > k.lo) k.lo = k.sl = k.nst = 0;
     k.n = k.nst + (k.last - k.lo) / BN + 1;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {

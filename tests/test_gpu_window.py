@@ -102,6 +102,26 @@ def test_short_windows_without_sinks(window, group):
         check(got, ref[n], n)
 
 
+@pytest.mark.parametrize("window, sink", [(1, 0), (1, 3), (1, 300), (129, 150), (129, 128), (128, 257), (100, 129),
+                                          (257, 400), (40, 1000), (1000, 7)])
+@pytest.mark.parametrize("tokens, group, pos0", [(390, 1, 0), (131, 3, 256)])
+def test_many_planes(tokens, group, pos0, window, sink):
+    """152 (sequence, KV head) planes: work items of two query tiles whose windows and sinks need
+    different key tiles."""
+    Tk = pos0 + tokens
+    g = torch.Generator(device="cuda")
+    g.manual_seed(10)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v = r(2, tokens, 76 * group, 64), r(2, 76, Tk, 64), r(2, 76, Tk, 64)
+    d_out = r(2, tokens, 76 * group, 64)
+    cfg = abi.window_config(2, tokens, Tk, 76 * group, 76, 64, 64, window, sink, pos0)
+    out, lse = abi.window_forward(cfg, q, k, v)
+    grads = abi.window_backward(cfg, q, k, v, out, lse, d_out)
+    ref = window_ref(q, k, v, visible(tokens, Tk, pos0, window, sink, "cuda"), cfg.scale, d_out)
+    for n, got in zip(("out", "lse", "dq", "dk", "dv"), (out, lse) + grads):
+        check(got, ref[n], n)
+
+
 def test_lse_is_optional_and_calls_repeat_bit_for_bit():
     cfg, x, d_out, _ = make("gqa16_192", seed=2)
     out, lse = abi.window_forward(cfg, **x)
