@@ -60,7 +60,10 @@ struct AppendArgs {
     int32_t* ref;
     int32_t* short_pages;
     int32_t* free_list;   // [n_pages]
-    int4* plan;           // [B] {length before, tokens (0: nothing to do), page to copy from or -1, 0}
+    // [B] {length before, tokens (0: nothing to do), page to copy from or -1, flag}.  A row that keeps
+    // a page writes behind its own tokens there.  Where a row that copies the page has more tokens
+    // of it, the copy has to come first: then both rows' flag is 1, and the keeper's CTAs do both.
+    int4* plan;
 };
 
 __device__ __forceinline__ int append_count(const AppendArgs& a, int b) {
@@ -68,7 +71,9 @@ __device__ __forceinline__ int append_count(const AppendArgs& a, int b) {
 }
 
 // Shared memory: tail[B] (the row's shared last page, or -1), begin[B] (rank of
-// its first new page).
+// its first new page; bit 31: it keeps its shared page), used[B] (rows of its last page).
+constexpr int APPEND_SMEM_ROW = 9;
+
 __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const AppendArgs a) {
     extern __shared__ int32_t sh[];
     __shared__ int warp_sums[32];
@@ -76,6 +81,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const AppendA
     const PagedShape& s = a.s;
     int32_t* tail = sh;
     int32_t* begin = sh + s.B;
+    uint8_t* used = reinterpret_cast<uint8_t*>(sh + 2 * s.B);       // below P <= 256
     pdl_launch();
     if (threadIdx.x == 0) over = 0;
     for (int b = threadIdx.x; b < s.B; b += PLAN_THREADS) {
@@ -86,6 +92,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const AppendA
             if ((unsigned)page >= (unsigned)s.n_pages || a.ref[page] < 2) page = -1;
         }
         tail[b] = page;
+        used[b] = (uint8_t)(L & (s.P - 1));
     }
     __syncthreads();
     // pages that each row takes; rows in order, PLAN_THREADS at a time
@@ -144,7 +151,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const AppendA
         const int have = (L + s.P - 1) >> s.logP, then = n > 0 ? (L + n + s.P - 1) >> s.logP : 0;
         const int col0 = copy ? have - 1 : have;
         const int32_t* mine = a.free_list + (begin[b] & 0x7FFFFFFF);
-        __syncwarp();
+        bool first = false;                         // copies have to come before the keeper's tokens
+        if (n > 0 && tail[b] >= 0)
+            for (int e = lane; e < s.B; e += 32)
+                first |= tail[e] == tail[b] && (copy ? begin[e] < 0 && used[e] < used[b]
+                                                     : begin[e] >= 0 && used[e] > used[b]);
+        first = __any_sync(0xffffffffu, first);
         for (int c = col0 + lane; c < then; c += 32) {
             const int page = mine[c - col0];
             a.table[(size_t)b * s.cols + c] = page;
@@ -152,7 +164,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) append_plan_kernel(const AppendA
         }
         if (lane == 0) {
             if (copy) atomicSub(&a.ref[tail[b]], 1);
-            a.plan[b] = make_int4(L, n, copy ? tail[b] : -1, 0);
+            a.plan[b] = make_int4(L, n, copy ? tail[b] : -1, first);
         }
         __syncwarp();
         if (lane == 0 && n > 0) a.lens[b] = L + n;
@@ -186,13 +198,31 @@ __global__ void __launch_bounds__(256) append_write_kernel(const AppendArgs a) {
     const int page = a.table[(size_t)b * s.cols + col];
     if ((unsigned)page >= (unsigned)s.n_pages) return;
     const size_t at = ((size_t)page * s.Hkv + h) * s.P;
-    if (j == 0 && plan.z >= 0) {
-        const size_t from = ((size_t)plan.z * s.Hkv + h) * s.P;
-        const int r = L & (s.P - 1);
-        copy_rows(reinterpret_cast<uint4*>(a.kp + at * s.dqk), reinterpret_cast<const uint4*>(a.kp + from * s.dqk),
+    // the r rows of page `from` that a row has, into its own page `to`
+    auto copy_page = [&](int from, int to, int r) {
+        const size_t f = ((size_t)from * s.Hkv + h) * s.P, t = ((size_t)to * s.Hkv + h) * s.P;
+        copy_rows(reinterpret_cast<uint4*>(a.kp + t * s.dqk), reinterpret_cast<const uint4*>(a.kp + f * s.dqk),
                   r * (s.dqk / 8));
-        copy_rows(reinterpret_cast<uint4*>(a.vp + at * s.dv), reinterpret_cast<const uint4*>(a.vp + from * s.dv),
+        copy_rows(reinterpret_cast<uint4*>(a.vp + t * s.dv), reinterpret_cast<const uint4*>(a.vp + f * s.dv),
                   r * (s.dv / 8));
+    };
+    if (j == 0 && plan.z >= 0 && !plan.w) copy_page(plan.z, page, L & (s.P - 1));
+    if (j == 0 && plan.z < 0 && plan.w) {           // the copies of this page that reach behind this row's end
+        __shared__ int rows[256], n_rows;
+        for (int e0 = 0; e0 < s.B; e0 += 256) {
+            __syncthreads();
+            if (threadIdx.x == 0) n_rows = 0;
+            __syncthreads();
+            const int e = e0 + threadIdx.x;
+            if (e < s.B && a.plan[e].w && a.plan[e].z == page) rows[atomicAdd(&n_rows, 1)] = e;
+            __syncthreads();
+            for (int i = 0; i < n_rows; ++i) {
+                const int Le = a.plan[rows[i]].x;
+                const int to = a.table[(size_t)rows[i] * s.cols + (Le >> s.logP)];
+                if ((unsigned)to < (unsigned)s.n_pages) copy_page(page, to, Le & (s.P - 1));
+            }
+        }
+        __syncthreads();                            // read, before the tokens below are written
     }
     const size_t src = ((size_t)b * s.Hkv + h) * s.Tq + (lo - L);
     const size_t dst = at + (lo & (s.P - 1));
@@ -366,12 +396,12 @@ cudaError_t launch_paged_append(const PagedShape& s, const __nv_bfloat16* k_new,
     AppendArgs a{s, k_new, v_new, n_new, kp, vp, table, lens, ref, short_pages, nullptr, nullptr};
     a.plan = reinterpret_cast<int4*>(ws);
     a.free_list = reinterpret_cast<int32_t*>(ws + up256((size_t)s.B * sizeof(int4)));
-    const int smem = s.B * 8;
+    const int smem = s.B * APPEND_SMEM_ROW;
     static std::atomic<bool> allowed[MAX_DEVICES];
     int dev;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = allow_smem(reinterpret_cast<const void*>(append_plan_kernel), APPEND_MAX_B * 8, dev, allowed);
+    e = allow_smem(reinterpret_cast<const void*>(append_plan_kernel), APPEND_MAX_B * APPEND_SMEM_ROW, dev, allowed);
     if (e != cudaSuccess) return e;
     append_plan_kernel<<<1, PLAN_THREADS, smem, st>>>(a);
     e = cudaGetLastError();

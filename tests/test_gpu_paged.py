@@ -163,6 +163,31 @@ def test_sharers_of_one_last_page():
         assert sum(r > 0 for r in c.ref) == used + copies
 
 
+@pytest.mark.parametrize("page", [16, 256])
+@pytest.mark.parametrize("keeper", [2, 0])
+def test_sharers_with_different_lengths_on_one_page(page, keeper):
+    """Rows share their last page with different lengths (some were shortened): the row that keeps
+    it, the last one, writes over what the others still copy.  Row 3 has another page, shared with 4."""
+    rows = 40
+    rng = random.Random(6)
+    c = filled(rows, 4, 4 * rows, page, 3, 192, 128, [2 * page - 1, 0, 0, page - 3, 0], seed=10)
+    x = c.on_gpu()
+    books = (x["table"], x["lens"], x["ref"])
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    cfg = abi.paged_config(rows, 1, 3, 3, 192, 128, page, 4 * rows, 4)
+    src, dst = [0] * (rows - 3) + [3], [b for b in range(1, rows) if b not in (3, 4)] + [4]
+    assert abi.pages_fork(cfg, i32(src), i32(dst), *books).tolist() == c.fork(src, dst)
+    some = [b for b in range(rows) if b not in (3, rows - 1)] + [rows - 1]
+    keep = [page + rng.randint(1, page - 1) if b != 4 else rng.randint(1, page - 4) for b in some[:-1]]
+    keep.append(page + 1 + keeper)
+    assert abi.pages_free(cfg, i32(some), *books, keep=i32(keep)).tolist() == c.free(some, keep)
+    cfg = abi.paged_config(rows, page, 3, 3, 192, 128, page, 4 * rows, 4)
+    k_new, v_new = c.new_tokens(rows, page)
+    assert int(abi.paged_append(cfg, k_new.cuda(), v_new.cuda(), x["k_pages"], x["v_pages"], *books)) == 0
+    assert c.append(k_new, v_new, [page] * rows) == 0
+    c.assert_equal(x)
+
+
 def test_n_new_null_appends_everything_and_a_full_pool_changes_nothing():
     c = filled(3, 8, 9, 16, 2, 128, 64, [20, 0, 16], seed=2)
     x = c.on_gpu()
