@@ -13,6 +13,16 @@ struct WinShape {
     float scale;
 };
 
+// The backward's weights are p = exp(s - lse) <= 1, but lse has 24 bits: at |lse| = 2^20 its last
+// place moves p by a tenth, from 2^31 on by more than fp32's range.  So where |lse| > LARGE_LSE the
+// exponent is clamped to 0, and lse enters lowered by 2^-20 of its size, more than the roundings
+// of lse and of the scores add up to (16 of 2^-24): a key that has all the weight gets p = 1.
+constexpr float LARGE_LSE = 4096.f;
+__device__ __forceinline__ float bwd_lse(float lse) {
+    return lse > LARGE_LSE ? lse * (1.f - 0x1p-20f) : lse < -LARGE_LSE ? lse * (1.f + 0x1p-20f) : lse;
+}
+__device__ __forceinline__ float at_most_0(float x) { return x > 0.f ? 0.f : x; }       // (NaN stays NaN)
+
 // Any shape: FFMA, one warp per row (window_rowwise.cu).  delta [B, Tq, Hq].
 cudaError_t launch_window_rowwise_fwd(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                       const __nv_bfloat16* v, __nv_bfloat16* out, float* lse, cudaStream_t st);

@@ -87,6 +87,7 @@ struct Bars {
     uint64_t acc_full, acc_free, aux_full[2], aux_empty[2], drain;
     uint32_t tmem;
     int abort;
+    int large;          // DKV: a row with |lse| > LARGE_LSE has been among the steps so far
 };
 
 // How the key tiles are cut into items (DKV): key tiles below nsk hold sinks
@@ -258,7 +259,7 @@ __device__ __forceinline__ void rows_delta(const Args& a, const Work& k, int r0,
     for (int e = 0; e < E; ++e) {
         if (32 * e + lane >= N) continue;
         float2* v = dst + 32 * e + lane;
-        v->x = ls[e] * LOG2E;
+        v->x = bwd_lse(ls[e]) * LOG2E;
         if (at[e] >= 0) a.delta[at[e]] = v->y;
     }
 }
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     Bars& bar = *reinterpret_cast<Bars*>(sm + L::BAR_OFF);
     float2* aux = reinterpret_cast<float2*>(sm + L::AUX_OFF);
     volatile int* abort_flag = &bar.abort;
+    volatile int* large = &bar.large;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WinShape& s = a.s;
     // What follows in the stream may start on the SMs that this grid leaves idle: of its
@@ -299,6 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc::mbar_init(&bar.acc_free, 8);
         tc::mbar_init(&bar.drain, 1);
         bar.abort = 0;
+        bar.large = 0;
         tc::fence_mbar_init();
         tc::prefetch_map(&map_r1);
         tc::prefetch_map(&map_r2);
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     v[e] = make_float2(3e38f, 0.f);             // p = 0: no query
                     if (tt[e] < a.tok && first + tt[e] < s.Tq) {
                         const size_t row = ((size_t)k.b * s.Tq + first + tt[e]) * s.Hq + k.kvh * s.G + head[e];
-                        v[e] = make_float2(a.lse[row], a.delta[row]);
+                        v[e] = make_float2(bwd_lse(a.lse[row]), a.delta[row]);
                     }
                 }
             };
@@ -580,6 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int r = lane + 32 * e, half = (r >> 2) & 1;
                     uint4* x = reinterpret_cast<uint4*>(sm + L::AUX_OFF + L::EXT_A + st * 2 * L::EXT_B + r * 32);
+                    if (fabsf(v[e].x) > LARGE_LSE && v[e].x != 3e38f) *large = 1;
                     // (of a row without a query: -3e38, not times 1 / scale, which could pass fp32)
                     x[half] = three(v[e].x == 3e38f ? -3e38f : -v[e].x * inv_scale);
                     x[half ^ 1] = make_uint4(0, 0, 0, 0);
@@ -607,7 +611,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (MODE == DQ) tile_rows.init(r, s.G);
         uint32_t g = 0, works = 0, n = 0;
         bool ok = true;
-        const uint64_t sc2 = tc::f2_pack(a.scale_log2, a.scale_log2);
         for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
             Work k;
             if (!decode_work<MODE>(a, w, &k)) continue;
@@ -626,9 +629,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) tc::mbar_arrive(&bar.aux_empty[buf]);
                 ++n;
             }
-            const uint64_t lse2 = tc::f2_pack(-mine.x, -mine.x), del2 = tc::f2_pack(-mine.y, -mine.y);
+            // exponents are scores times sc2 + lse2, or, where a large lse could lift them above 0, taken
+            // and clamped beforehand
+            bool clamp = MODE == DQ && __any_sync(0xffffffffu, fabsf(mine.x) > LARGE_LSE);
+            uint64_t sc2 = clamp ? tc::f2_pack(1.f, 1.f) : tc::f2_pack(a.scale_log2, a.scale_log2);
+            const float neg = clamp ? 0.f : -mine.x;
+            const uint64_t lse2 = tc::f2_pack(neg, neg), del2 = tc::f2_pack(-mine.y, -mine.y);
             for (int i = 0; i < k.n; ++i, ++g) {
                 if ((int)(g & 1) != wg) continue;
+                if (MODE == DKV) {
+                    // (not reused before this step's P is read: makes the flag of its rows visible)
+                    if (!warp_wait(&bar.t_full[g % L::NST], (g / L::NST) & 1)) { ok = false; break; }
+                    clamp = *large != 0;
+                    sc2 = clamp ? tc::f2_pack(1.f, 1.f) : tc::f2_pack(a.scale_log2, a.scale_log2);
+                }
                 if (!warp_wait(&bar.s_full[wg], (g >> 1) & 1)) { ok = false; break; }
                 tc::fence_after_sync();
                 uint32_t x[64], y[64];
@@ -654,13 +668,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 tc::tmem_wait_ld();
                 const bool full = hi >= BN - 1 && (lo <= 0 || sk >= BN);
-                if (!__all_sync(0xffffffffu, full)) {
+                if (!__all_sync(0xffffffffu, full && !clamp)) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const uint32_t bits = range_bits(lo, hi, c) | range_bits(0, sk - 1, c);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!((bits >> e) & 1u)) x[32 * c + e] = 0xFF800000u;
+                    }
+                    if (clamp) {                    // (bwd_lse)
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            x[c] = __float_as_uint(at_most_0(fmaf(__uint_as_float(x[c]), a.scale_log2, -mine.x)));
                     }
                 }
                 // (DKV: mine = 0, S and D carry the queries' lse and delta)

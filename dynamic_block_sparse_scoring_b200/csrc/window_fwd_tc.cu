@@ -52,6 +52,11 @@ constexpr int BM = 128, BN = 128;
 constexpr int CHUNK = 16384;                    // 128 rows x 64 columns of bf16
 constexpr int THREADS = 384;
 constexpr uint64_t WAIT_NS = 1000000000ull;
+// From this |m| on a row takes the largest power of two below scale log2 e for its scale.  The weights
+// 2^(fma(s, c2, -m)) carry the rounding of m, up to here 2^5 at most: a power that O and l share.
+// From here on it would pass fp32's range, so m = maximum 2^i is exact; and as different scores are 2^5
+// or more apart, a smaller scale moves no weight by more than 2^-32.
+constexpr float LARGE_REF = 1073741824.f;
 
 template <int DQK, int DV>
 struct Smem {
@@ -356,14 +361,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ns = 0, no = 0;
         bool ok = true;
         auto warp_wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
-        const uint64_t sc2 = tc::f2_pack(a.scale_log2, a.scale_log2);
+        const float pow2_log2 = __uint_as_float(__float_as_uint(a.scale_log2) & 0x7F800000u);
         for (int w = blockIdx.x; ok && w < a.n_work; w += gridDim.x) {
             const Work k = decode_work(a, w);
             if (t >= k.nt) continue;
             const int pos = (t ? k.pf[1] : k.pf[0]) + tt;
             const bool row_ok = tt < a.tok && pos < s.q0 + s.Tq;
             const int kc = t ? k.c[1] : k.c[0], kf = t ? k.f[1] : k.f[0], ke = t ? k.e[1] : k.e[0];
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, c2 = a.scale_log2;        // m = maximum c2 (LARGE_REF)
             for (int j = kc > 0 ? 0 : kf, first = 1; j < ke; first = 0, j = j + 1 < kc ? j + 1 : max(j + 1, kf)) {
                 const int u0 = k.key(j), nc = k.width(j) >> 5;
                 // visible offsets: [lo, hi] and, behind the window, [0, sk)
@@ -415,12 +420,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (full) load(std::false_type{});
                 else load(std::true_type{});
                 // scale > 0, so the scaled maximum is the maximum of the scaled scores
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float mt = __fmul_rn(top, c2);                  // (not fused with a difference: the weights' reference)
                 float alpha = 1.f;                              // for what was summed under the reference before
                 if (mt > m + 8.f || m == -INFINITY) {           // (-inf > -inf is false: m stays)
+                    c2 = fabsf(top * a.scale_log2) < LARGE_REF ? a.scale_log2 : pow2_log2;
+                    mt = __fmul_rn(top, c2);
                     if (m != -INFINITY) alpha = tc::ex2(m - mt);
                     m = mt;
                 }
+                const uint64_t sc2 = tc::f2_pack(c2, c2);
                 const float neg = m == -INFINITY ? 0.f : -m;
                 const uint64_t neg2 = tc::f2_pack(neg, neg);
                 uint64_t sum[2] = {0, 0};
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (row_ok && a.lse)
                 a.lse[((size_t)k.b * s.Tq + (pos - s.q0)) * s.Hq + k.kvh * s.G + g] =
-                    (m + log2f(l)) * 0.6931471805599453f;
+                    c2 == a.scale_log2 ? (m + log2f(l)) * 0.6931471805599453f : fmaf(m, s.scale / c2, logf(l));
             tc::fence_before_sync();
         }
         if (!ok) give_up();

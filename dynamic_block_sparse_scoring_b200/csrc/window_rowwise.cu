@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(128) window_fwd_kernel(WinShape s, const __nv_
         float mx = m;
 #pragma unroll
         for (int j = 0; j < KU; ++j) {
-            sc[j] = j < n ? warp_sum(sc[j]) * s.scale : -INFINITY;
+            sc[j] = j < n ? __fmul_rn(warp_sum(sc[j]), s.scale) : -INFINITY;   // (the maximum's weight is 1)
             mx = fmaxf(mx, sc[j]);
         }
         const float alpha = expf(m - mx);
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(128) window_dq_kernel(WinShape s, const __nv_b
     load_row(out + (size_t)w * s.dv, nv, lane, acc);
     load_row(d_out + (size_t)w * s.dv, nv, lane, df);
     load_row(q + (size_t)w * s.dqk, nq, lane, qf);
-    const float dl = warp_sum(dot(acc, df)), ls = lse[w];
+    const float dl = warp_sum(dot(acc, df)), ls = bwd_lse(lse[w]);
     if (lane == 0) delta[w] = dl;
 #pragma unroll
     for (int i = 0; i < MAXP; ++i) acc[i] = make_float2(0.f, 0.f);
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(128) window_dq_kernel(WinShape s, const __nv_b
             float2 kf[MAXP], vf[MAXP];
             load_row(k + (r.plane * s.Tk + u0 + j) * s.dqk, nq, lane, kf);
             load_row(v + (r.plane * s.Tk + u0 + j) * s.dv, nv, lane, vf);
-            const float p = expf(warp_sum(dot(qf, kf)) * s.scale - ls);
+            const float p = expf(at_most_0(warp_sum(dot(qf, kf)) * s.scale - ls));
             const float ds = p * (warp_sum(dot(df, vf)) - dl);
 #pragma unroll
             for (int i = 0; i < MAXP; ++i)
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(128) window_dkv_kernel(WinShape s, const __nv_
             float2 qf[MAXP], df[MAXP];
             load_row(q + row * s.dqk, nq, lane, qf);
             load_row(d_out + row * s.dv, nv, lane, df);
-            const float p = expf(warp_sum(dot(qf, kf)) * s.scale - lse[row]);
+            const float p = expf(at_most_0(warp_sum(dot(qf, kf)) * s.scale - bwd_lse(lse[row])));
             const float ds = p * (warp_sum(dot(df, vf)) - delta[row]);
 #pragma unroll
             for (int i = 0; i < MAXP; ++i) {

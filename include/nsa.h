@@ -349,7 +349,8 @@ typedef struct {
  * enter the value product rounded to bf16 (relative 2^-8 at most, half a step)
  * while their sum is taken unrounded; other shapes run on FFMA without that
  * rounding.  k and v must be finite at every row of the cache, masked rows
- * included: a masked key enters the value product with weight 0.
+ * included: a masked key enters the value product with weight 0.  Scores of
+ * any size are served as long as |scale q.k| stays below 1e38.
  * Needs no workspace.
  */
 nsa_status nsa_window_attn_fwd(const nsa_window_config* cfg, const void* q, const void* k, const void* v,
@@ -363,6 +364,9 @@ nsa_status nsa_window_attn_fwd(const nsa_window_config* cfg, const void* q, cons
  *   dk [B, Hkv, Tkv, d_qk] = scale sum_{t, h} ds_u q      dv_u = sum_{t, h} p_u d_out
  * all bf16 and overwritten (rows of dk / dv that no query sees get 0), summed
  * in fp32 over the group's heads and every query and rounded once at the end.
+ * p is rebuilt from lse, whose 24 bits move it by a relative |lse| 2^-20 at
+ * most (half a bf16 step at |lse| = 2^12); p stays in [0, 1] whatever the
+ * scores, and a key that has a row's whole weight keeps it.
  * No atomics: the same inputs give the same bits.  Needs
  * nsa_window_bwd_workspace_size() bytes of workspace (delta, and the partial
  * sums of keys that many queries see); nothing in it needs to start at zero.

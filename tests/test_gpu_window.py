@@ -264,3 +264,22 @@ def test_offsets_past_32_bits():
     for n, x in [("out", out), ("lse", lse), ("dq", dq), ("dk", near(dk)), ("dv", near(dv))]:
         check(x, ref[n], n)
     assert not dk[:, :, ns:far].any() and not dv[:, :, ns:far].any()
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (256, 256)], ids=str)
+def test_a_query_that_is_not_a_number_shows_in_every_output(dims):
+    """A NaN is not clamped away: its row's out, lse and dq and its keys' dk and dv are NaN."""
+    dqk, dv = dims
+    g = torch.Generator(device="cuda")
+    g.manual_seed(14)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, d_out = r(1, 90, 4, dqk), r(1, 2, 90, dqk), r(1, 2, 90, dv), r(1, 90, 4, dv)
+    q[0, 50, 1, 3] = float("nan")
+    q[0, 20, 0] *= 4096                             # a large score in the same group
+    cfg = abi.window_config(1, 90, 90, 4, 2, dqk, dv, 8, 0)
+    out, lse = abi.window_forward(cfg, q, k, v)
+    dq, dk, dvv = abi.window_backward(cfg, q, k, v, out, lse, d_out)
+    for x in (out, lse.unsqueeze(-1), dq):
+        assert x[0, 50, 1].isnan().all() and x[0, 50, 0].isfinite().all() and x[0, 49, 1].isfinite().all()
+    for x in (dk, dvv):
+        assert x[0, 0, 43:51].isnan().any(-1).all() and x[0, 1].isfinite().all()
