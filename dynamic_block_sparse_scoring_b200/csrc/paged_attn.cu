@@ -14,8 +14,9 @@
 //   S = Q K^T (16 x 16), p = exp2(S - m) under the running row maximum m,
 //   O = O exp2(m_old - m) + P V, l += sum p.
 // A unit inside one share is finished there; a unit cut by shares leaves one
-// (O / l, m + log2 l) per share, joined by paged_join_kernel:
-//   lse = log2 sum_i 2^lse_i,  o = sum_i 2^(lse_i - lse) o_i.
+// (O / l, m, l) per share, joined by paged_join_kernel under the largest m, M:
+//   w_i = 2^(m_i - M) l_i,  o = sum_i w_i o_i / sum_i w_i,  lse = M + log2 sum_i w_i.
+// (m and l apart: in m + log2 l a large m would swallow the sum.)
 // mma.sync rather than tcgen05: with the group's 1-16 heads as M the products
 // need a few percent of the tensor cores at full HBM rate, and a warp keeps
 // its whole state in registers, without a CTA-wide hand-over per tile.
@@ -82,7 +83,7 @@ struct PagedArgs {
     __nv_bfloat16* out;
     float* lse;
     float* part_o;          // [2 * workers][ROWS][dv]
-    float* part_lse;        // [2 * workers][ROWS]
+    float2* part_ml;        // [2 * workers][ROWS] running maximum and sum
     int RT;                 // row tiles per (sequence, KV head)
     float scale_log2;
 };
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
                 float x[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    x[j] = sc[j >> 1][2 * e + (j & 1)] * a.scale_log2;
+                    x[j] = __fmul_rn(sc[j >> 1][2 * e + (j & 1)], a.scale_log2);    // (the maximum's weight is 1)
                     if (!all) {
                         const int u = u0 + (j >> 1) * 8 + qc + (j & 1);
                         const bool vis = u <= trow[e] && (s.win == 0 || u > trow[e] - s.win || u < s.ns);
@@ -379,19 +380,19 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
         for (int e = 0; e < 2; ++e) {
             if (!rok[e]) continue;
             const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
-            const float ls2 = l[e] > 0.f ? m[e] + log2f(l[e]) : -INFINITY;
             if (whole) {
                 uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow[e] * DV + qc);
 #pragma unroll
                 for (int n = 0; n < DV / 8; ++n)
                     dst[n * 4] = tc::pack_bf16x2(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
-                if (a.lse && (lane & 3) == 0) a.lse[orow[e]] = ls2 * 0.6931471805599453f;
+                if (a.lse && (lane & 3) == 0)
+                    a.lse[orow[e]] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.6931471805599453f : -INFINITY;
             } else {
                 const size_t pr = (size_t)slot * ROWS + qr + 8 * e;
                 float2* dst = reinterpret_cast<float2*>(a.part_o + pr * DV + qc);
 #pragma unroll
                 for (int n = 0; n < DV / 8; ++n) dst[n * 4] = make_float2(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
-                if ((lane & 3) == 0) a.part_lse[pr] = ls2;
+                if ((lane & 3) == 0) a.part_ml[pr] = make_float2(m[e], l[e]);
             }
         }
         g += i1 - i0;
@@ -459,20 +460,19 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const Paged
     for (int c = 0; c < NC; ++c) acc[c] = make_float2(0.f, 0.f);
     constexpr int U = 8, STEP = SPLIT ? JOIN_WARPS : 1;
     for (int w = w0 + (SPLIT ? warp : 0); w <= w1; w += U * STEP) {
-        float ls[U];
-        float2 x[U][NC];
+        float2 ml[U], x[U][NC];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool ok = w + u * STEP <= w1;
             const size_t pr = part_row(ok ? w + u * STEP : w);
-            ls[u] = ok ? a.part_lse[pr] : -INFINITY;
+            ml[u] = ok ? a.part_ml[pr] : make_float2(-INFINITY, 0.f);
 #pragma unroll
             for (int c = 0; c < NC; ++c)
                 x[u][c] = ok ? reinterpret_cast<const float2*>(a.part_o + pr * DV)[c * 32 + lane] : make_float2(0.f, 0.f);
         }
         float top = mx;
 #pragma unroll
-        for (int u = 0; u < U; ++u) top = fmaxf(top, ls[u]);
+        for (int u = 0; u < U; ++u) top = fmaxf(top, ml[u].x);
         const float ref = top == -INFINITY ? 0.f : top, old = tc::ex2(mx - ref);
         mx = top;
         sum *= old;
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const Paged
         for (int c = 0; c < NC; ++c) acc[c] = make_float2(acc[c].x * old, acc[c].y * old);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float wt = tc::ex2(ls[u] - ref);
+            const float wt = tc::ex2(ml[u].x - ref) * ml[u].y;
             sum += wt;
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -549,7 +549,7 @@ cudaError_t launch_impl(PagedArgs a, int n_units, int rows, cudaStream_t st) {
 }  // namespace
 
 size_t paged_attn_ws_bytes(const PagedShape& s) {
-    return up256((size_t)2 * MAX_WORKERS * ROWS * s.dv * 4) + up256((size_t)2 * MAX_WORKERS * ROWS * 4);
+    return up256((size_t)2 * MAX_WORKERS * ROWS * s.dv * 4) + (size_t)2 * MAX_WORKERS * ROWS * sizeof(float2);
 }
 
 cudaError_t launch_paged_attn(const PagedShape& s, const __nv_bfloat16* q, const __nv_bfloat16* kp,
@@ -566,7 +566,7 @@ cudaError_t launch_paged_attn(const PagedShape& s, const __nv_bfloat16* q, const
     a.lse = lse;
     a.part_o = reinterpret_cast<float*>(ws);
     ws += up256((size_t)2 * MAX_WORKERS * ROWS * s.dv * 4);
-    a.part_lse = reinterpret_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws);
     const int rows = s.Tq * s.G;
     a.RT = (rows + ROWS - 1) / ROWS;
     a.scale_log2 = s.scale * 1.4426950408889634f;

@@ -12,6 +12,7 @@ import pytest
 import torch
 
 from dynamic_block_sparse_scoring_b200 import abi
+from tests.paged_ref import filled
 from tests.window_ref import check, visible, window_ref
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +109,24 @@ def test_backward_weights_stay_below_one(dims, scale):
     ref = window_ref(q, k, v, vis, cfg.scale, d_out)["dv"][0]
     size = window_ref(q, k, v, vis, cfg.scale, d_out.abs())["dv"][0]           # sum p|d_out|
     check(got[2], (ref, (2 * H + 2.0 ** -16) * size + 1e-6), "dv")
+
+
+@pytest.mark.parametrize("scale", [1e6, 1e9, 1e30])
+@pytest.mark.parametrize("new, page, lens", [(1, 16, [700, 3, 64]), (3, 64, [2100])])
+def test_paged_attention_gives_the_weight_to_the_largest_scores(scale, new, page, lens):
+    cols = -(-max(lens) // page) + 1
+    c = filled(len(lens), cols, sum(-(-n // page) for n in lens) + 2, page, 2, 128, 128, lens, 24)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(24)
+    c.k = torch.where(c.k.isnan(), c.k, c.k.float().round().clamp(-1, 1).to(torch.bfloat16))
+    x = c.on_gpu()
+    q = _whole(g, -1, 1, len(lens), new, 8, 128)
+    cfg = abi.paged_config(len(lens), new, 8, 2, 128, 128, page, len(c.ref), cols, scale=scale)
+    out, lse = abi.paged_attention(cfg, q, x["k_pages"], x["v_pages"], x["table"], x["lens"])
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    for b, n in enumerate(lens):
+        k, v = (y.unsqueeze(0).cuda() for y in c.dense(b))
+        vis = visible(new, n, n - new, 1 << 30, 0, "cuda")
+        ref = _bounded(window_ref(q[b:b + 1], k, v, vis, cfg.scale), q[b:b + 1], k, v, vis, cfg.scale)
+        check(out[b:b + 1], ref["out"], f"row {b} out")
+        check(lse[b:b + 1], ref["lse"], f"row {b} lse")
