@@ -379,14 +379,14 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (!rok[e]) continue;
-            const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+            const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
             if (whole) {
                 uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow[e] * DV + qc);
 #pragma unroll
                 for (int n = 0; n < DV / 8; ++n)
                     dst[n * 4] = tc::pack_bf16x2(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
                 if (a.lse && (lane & 3) == 0)
-                    a.lse[orow[e]] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.6931471805599453f : -INFINITY;
+                    a.lse[orow[e]] = l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * 0.6931471805599453f;
             } else {
                 const size_t pr = (size_t)slot * ROWS + qr + 8 * e;
                 float2* dst = reinterpret_cast<float2*>(a.part_o + pr * DV + qc);
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const Paged
             wt[w] = mx == -INFINITY ? 0.f : tc::ex2(ml_s[w].x - mx);
             sum = fmaf(wt[w], ml_s[w].y, sum);
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         for (int c = threadIdx.x; c < DV / 2; c += JOIN_WARPS * 32) {
             float x = 0.f, y = 0.f;
 #pragma unroll
@@ -514,12 +514,12 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const Paged
             dst[c] = tc::pack_bf16x2(x * inv, y * inv);
         }
     } else {
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int c = 0; c < NC; ++c) dst[c * 32 + lane] = tc::pack_bf16x2(acc[c].x * inv, acc[c].y * inv);
     }
     if (a.lse && lane == 0 && (!SPLIT || warp == 0))
-        a.lse[orow] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        a.lse[orow] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }

@@ -340,3 +340,20 @@ def test_two_streams_with_workspaces_of_their_own():
     for w, many in zip(want, got):
         for o, l in many:
             assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+@pytest.mark.parametrize("lens, h_q", [([40, 7], 8), ([5000, 7], 8), ([5000, 7], 2)])
+def test_a_key_that_is_not_a_number_shows_in_out_and_lse(lens, h_q):
+    """One NaN among a row's keys, in a unit that one warp finishes and in one that is cut and joined:
+    the row's out and lse are NaN (not -inf, which stands for no key), the other rows' are as before."""
+    c = filled(2, 80, 90, 64, 2, 128, 128, lens, seed=12)
+    cfg = abi.paged_config(2, 1, h_q, 2, 128, 128, 64, 90, 80)
+    q = torch.randn(2, 1, h_q, 128, generator=torch.Generator().manual_seed(13)).to(torch.bfloat16).cuda()
+    x = c.on_gpu()
+    want = abi.paged_attention(cfg, q, x["k_pages"], x["v_pages"], x["table"], x["lens"])
+    x["k_pages"][c.table[0][0], 0, 3, 5] = float("nan")              # KV head 0 of row 0
+    out, lse = abi.paged_attention(cfg, q, x["k_pages"], x["v_pages"], x["table"], x["lens"])
+    G = h_q // 2
+    assert out[0, :, :G].isnan().all() and lse[0, :, :G].isnan().all()
+    assert torch.equal(out[0, :, G:], want[0][0, :, G:]) and torch.equal(lse[0, :, G:], want[1][0, :, G:])
+    assert torch.equal(out[1], want[0][1]) and torch.equal(lse[1], want[1][1])
