@@ -666,7 +666,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     lo = max(min(pos - tb, BN), -BN) * s.G;
                     hi = pos < s.ns ? BN - 1 : max(min(pos - tb + s.win, BN), -BN) * s.G - 1;
                 }
-                tc::tmem_wait_ld();
+                tc::tmem_wait_ld32(x);
+                tc::tmem_wait_ld32(x + 32);
                 const bool full = hi >= BN - 1 && (lo <= 0 || sk >= BN);
                 if (!__all_sync(0xffffffffu, full && !clamp)) {
 #pragma unroll
@@ -695,7 +696,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::fence_after_sync();
                 tc::tmem_ld32(tD, y);
                 tc::tmem_ld32(tD + 32, y + 32);
-                tc::tmem_wait_ld();
+                tc::tmem_wait_ld32(y);
+                tc::tmem_wait_ld32(y + 32);
                 if (L::ND == 1) {
                     tc::fence_before_sync();
                     __syncwarp();

@@ -160,3 +160,15 @@ def test_wrappers_refuse_host_tensors(abi):
     k = torch.zeros(2, 2, 96, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         abi.window_forward(_win(abi), q, k, k)
+
+
+def test_waits_for_tensor_memory_name_the_registers():
+    """A load from tensor memory is asynchronous, and only a wait that names its registers keeps the
+    compiler from moving their uses before it: the window kernels use no other."""
+    import pathlib
+
+    import dynamic_block_sparse_scoring_b200 as pkg
+    for src in pathlib.Path(pkg.__file__).parent.joinpath("csrc").glob("window_*.cu"):
+        text = src.read_text()
+        assert "tmem_wait_ld()" not in text, src.name
+        assert "tmem_ld32(" not in text or "tmem_wait_ld32(" in text, src.name
