@@ -629,7 +629,10 @@ nsa_status nsa_check_bounded_wait(uint64_t limit_ns, void* stream) {
 
 nsa_status nsa_set_wait_limit_ns(uint64_t limit_ns) {
     if (limit_ns > 1000000000ull) return NSA_ERR_INVALID_ARG;
-    return cuda_status(nsa::set_wait_limit(limit_ns));
+    nsa_status st = cuda_status(nsa::set_wait_limit(limit_ns));
+    if (st == NSA_OK) st = cuda_status(nsa::set_win_fwd_wait_limit(limit_ns));
+    if (st == NSA_OK) st = cuda_status(nsa::set_win_bwd_wait_limit(limit_ns));
+    return st;
 }
 
 nsa_status nsa_timing_enable(int32_t on) {

@@ -36,6 +36,7 @@ bool window_tc_supported(const WinShape& s);
 cudaError_t launch_window_fwd_tc(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
                                  const __nv_bfloat16* v, __nv_bfloat16* out, float* lse, cudaStream_t st);
 int read_and_clear_win_fwd_status();
+cudaError_t set_win_fwd_wait_limit(uint64_t limit_ns);      // 0: one second
 // Backward for the same shapes (window_bwd_tc.cu); part: window_bwd_tc_part_bytes().
 size_t window_bwd_tc_part_bytes(const WinShape& s);
 cudaError_t launch_window_bwd_tc(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
@@ -43,4 +44,5 @@ cudaError_t launch_window_bwd_tc(const WinShape& s, const __nv_bfloat16* q, cons
                                  const __nv_bfloat16* d_out, __nv_bfloat16* dq, __nv_bfloat16* dk,
                                  __nv_bfloat16* dv, float* delta, float* part, cudaStream_t st);
 int read_and_clear_win_bwd_status();
+cudaError_t set_win_bwd_wait_limit(uint64_t limit_ns);
 }  // namespace nsa

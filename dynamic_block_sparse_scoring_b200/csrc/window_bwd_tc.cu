@@ -48,6 +48,8 @@
 namespace nsa {
 
 __device__ int g_win_bwd_status = 0;
+// Limit of the roles' waits (WAIT_NS unless nsa_set_wait_limit_ns shortened it); the drains keep WAIT_NS.
+__constant__ uint64_t c_win_bwd_wait_ns = 1000000000ull;
 
 namespace {
 
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = bar.tmem;
-    auto wait = [&](uint64_t* b, uint32_t parity) { return tc::mbar_wait(b, parity, abort_flag, WAIT_NS); };
+    auto wait = [&](uint64_t* b, uint32_t parity) { return tc::mbar_wait(b, parity, abort_flag, c_win_bwd_wait_ns); };
     auto warp_wait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
     auto give_up = [&]() {
         *abort_flag = 1;
@@ -385,12 +387,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (!ok) give_up();
-            // every copy issued here has landed before the CTA ends
+            // every copy issued here has landed before the CTA ends (one limit for all: t_full never
+            // completes where the warps that fill its other half have given up)
+            const uint64_t t0 = tc::globaltimer_ns();
+            auto drain = [&](uint64_t* b, uint32_t parity) {
+                const uint64_t used = tc::globaltimer_ns() - t0;
+                tc::mbar_wait_bounded(b, parity, used < WAIT_NS ? WAIT_NS - used : 0);
+            };
+            if (nr > 0) drain(&bar.r_full, (nr - 1) & 1);
             for (uint32_t i = 0; i < L::NST && i < g; ++i) {
                 const uint32_t last = i + ((g - 1 - i) / L::NST) * L::NST;
-                tc::mbar_wait_bounded(&bar.t_full[i], (last / L::NST) & 1, WAIT_NS);
+                drain(&bar.t_full[i], (last / L::NST) & 1);
             }
-            if (nr > 0) tc::mbar_wait_bounded(&bar.r_full, (nr - 1) & 1, WAIT_NS);
         } else if (warp == 1) {
             // ------------------------------------------------ MMA issue
             // The whole warp walks the schedule, one lane issues: the operands stay in
@@ -937,6 +945,11 @@ cudaError_t launch_window_bwd_tc(const WinShape& s, const __nv_bfloat16* q, cons
     NSA_WIN_CASE(192, 128)
 #undef NSA_WIN_CASE
     return cudaErrorInvalidValue;
+}
+
+cudaError_t set_win_bwd_wait_limit(uint64_t limit_ns) {
+    const uint64_t v = limit_ns ? limit_ns : WAIT_NS;
+    return cudaMemcpyToSymbol(c_win_bwd_wait_ns, &v, sizeof(v));
 }
 
 int read_and_clear_win_bwd_status() {

@@ -45,6 +45,8 @@
 namespace nsa {
 
 __device__ int g_win_fwd_status = 0;
+// Limit of the roles' waits (WAIT_NS unless nsa_set_wait_limit_ns shortened it); the drains keep WAIT_NS.
+__constant__ uint64_t c_win_fwd_wait_ns = 1000000000ull;
 
 namespace {
 
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = bar.tmem;
-    auto wait = [&](uint64_t* b, uint32_t parity) { return tc::mbar_wait(b, parity, abort_flag, WAIT_NS); };
+    auto wait = [&](uint64_t* b, uint32_t parity) { return tc::mbar_wait(b, parity, abort_flag, c_win_fwd_wait_ns); };
     auto give_up = [&]() {
         *abort_flag = 1;
         atomicExch(&g_win_fwd_status, (int)NSA_ERR_TIMEOUT);
@@ -549,6 +551,11 @@ cudaError_t launch_window_fwd_tc(const WinShape& s, const __nv_bfloat16* q, cons
     NSA_WIN_CASE(192, 128)
 #undef NSA_WIN_CASE
     return cudaErrorInvalidValue;
+}
+
+cudaError_t set_win_fwd_wait_limit(uint64_t limit_ns) {
+    const uint64_t v = limit_ns ? limit_ns : WAIT_NS;
+    return cudaMemcpyToSymbol(c_win_fwd_wait_ns, &v, sizeof(v));
 }
 
 int read_and_clear_win_fwd_status() {

@@ -505,8 +505,8 @@ nsa_status nsa_check_bounded_wait(uint64_t limit_ns, void* stream);
  * Test and debug knob (the pages have no counterpart): the limit, in ns, of
  * every bounded wait of the tensor-core attention kernel launched after this
  * call (the kernel behind nsa_sparse_attn_fwd's query-major, block-major and
- * split-K plans); 0 restores the default of one second, values above 1e9 are
- * refused.  With a limit shorter than the copies and MMAs take, the kernel's
+ * split-K plans) and of the window attention's tensor-core kernels; 0 restores
+ * the default of one second, values above 1e9 are refused.  With a limit shorter than the copies and MMAs take, the kernel's
  * waits give up: it raises NSA_ERR_TIMEOUT in the status word, every role
  * unwinds (the two warps that share rows leave their barriers together) and
  * the context stays usable.  The waits that drain in-flight copies and MMAs
