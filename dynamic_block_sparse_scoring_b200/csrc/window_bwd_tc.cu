@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WinShape& s = a.s;
     // What follows in the stream may start on the SMs that this grid leaves idle: of its
-    // results the DKV kernel reads delta alone, and waits for it.
+    // results the DKV kernel reads delta alone, and waits for it.  There every role waits for this
+    // grid's end before its first wait that needs delta, so that the bounded waits count the
+    // time of their own grid only; the copies of the first stages go before.
     pdl_launch();
 
     if (threadIdx.x == 0) {
@@ -352,6 +354,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 Work k;
                 if (!decode_work<MODE>(a, w, &k) || k.n == 0) continue;
                 const int plane = k.b * s.Hkv + k.kvh, h0 = k.kvh * s.G;
+                if (MODE == DKV && nr == 1) pdl_wait();
                 if (!wait(&bar.r_empty, (nr & 1) ^ 1)) { ok = false; break; }
                 tc::mbar_arrive_expect_tx(&bar.r_full, r_bytes);
 #pragma unroll
@@ -364,6 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++nr;
                 for (int i = 0; i < k.n; ++i, ++g) {
                     const int st = g % L::NST;
+                    if (MODE == DKV && g == L::NST) pdl_wait();
                     if (!wait(&bar.t_empty[st], ((g / L::NST) & 1) ^ 1)) { ok = false; break; }
                     tc::mbar_arrive_expect_tx(&bar.t_full[st], t_bytes);
                     uint8_t* dst = sm + L::T_OFF + st * L::T_BYTES;
@@ -387,6 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             if (!ok) give_up();
+            if (MODE == DKV) pdl_wait();
             // every copy issued here has landed before the CTA ends (one limit for all: t_full never
             // completes where the warps that fill its other half have given up)
             const uint64_t t0 = tc::globaltimer_ns();
@@ -419,6 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // needed, and waited for only if it was not there yet.
             auto soon = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, tc::mbar_test(b, parity)); };
             bool t_soon = false;
+            if (MODE == DKV) pdl_wait();
             // S and D of step g; p_bar: the barrier that is needed next (null: none), *p_soon: it is there
             auto scores = [&](uint64_t* p_bar, uint32_t p_parity, bool* p_soon) {
                 const uint32_t e = g, b = e & 1;
@@ -619,6 +625,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (MODE == DQ) tile_rows.init(r, s.G);
         uint32_t g = 0, works = 0, n = 0;
         bool ok = true;
+        if (MODE == DKV) pdl_wait();
         for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
             Work k;
             if (!decode_work<MODE>(a, w, &k)) continue;
