@@ -6,6 +6,7 @@
 namespace nsa {
 
 inline bool aligned16(const void* p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool supported_dqk(int d) { return d == 64 || d == 128 || d == 192 || d == 256; }
 inline bool supported_dv(int d) { return d == 64 || d == 128 || d == 256; }
 

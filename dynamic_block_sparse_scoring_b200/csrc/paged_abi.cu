@@ -8,6 +8,7 @@ namespace {
 
 using nsa::PagedShape;
 using nsa::aligned16;
+using nsa::aligned4;
 using nsa::cuda_status;
 
 nsa_status make_paged_shape(const nsa_paged_config* cfg, PagedShape* s) {
@@ -96,7 +97,8 @@ nsa_status nsa_paged_append(const nsa_paged_config* cfg, const void* k_new, cons
     if (!k_new || !v_new || !k_pages || !v_pages || !table || !lens || !ref || !short_pages)
         return NSA_ERR_INVALID_ARG;
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(n_new) || !aligned16(k_pages) ||
-        !aligned16(v_pages) || !aligned16(table) || !aligned16(lens) || !aligned16(ref) || !aligned16(workspace))
+        !aligned16(v_pages) || !aligned16(table) || !aligned16(lens) || !aligned16(ref) ||
+        !aligned4(short_pages) || !aligned16(workspace))
         return NSA_ERR_INVALID_ARG;
     if (s.B > nsa::APPEND_MAX_B) return NSA_ERR_UNSUPPORTED;
     if (!workspace || ws_bytes < nsa::paged_append_ws_bytes(s)) return NSA_ERR_WORKSPACE;
@@ -112,8 +114,9 @@ nsa_status nsa_pages_fork(const nsa_paged_config* cfg, int32_t n, const int32_t*
     nsa_status st = make_paged_shape(cfg, &s);
     if (st != NSA_OK) return st;
     if (n < 0 || !table || !lens || !ref) return NSA_ERR_INVALID_ARG;
+    if (!aligned16(table) || !aligned16(lens) || !aligned16(ref)) return NSA_ERR_INVALID_ARG;
     if (n == 0) return NSA_OK;
-    if (!src || !dst || !done) return NSA_ERR_INVALID_ARG;
+    if (!src || !dst || !done || !aligned4(src) || !aligned4(dst) || !aligned4(done)) return NSA_ERR_INVALID_ARG;
     return cuda_status(
         nsa::launch_pages_fork(s, n, src, dst, table, lens, ref, done, static_cast<cudaStream_t>(stream)));
 }
@@ -124,8 +127,9 @@ nsa_status nsa_pages_free(const nsa_paged_config* cfg, int32_t n, const int32_t*
     nsa_status st = make_paged_shape(cfg, &s);
     if (st != NSA_OK) return st;
     if (n < 0 || !table || !lens || !ref) return NSA_ERR_INVALID_ARG;
+    if (!aligned16(table) || !aligned16(lens) || !aligned16(ref)) return NSA_ERR_INVALID_ARG;
     if (n == 0) return NSA_OK;
-    if (!rows || !done) return NSA_ERR_INVALID_ARG;
+    if (!rows || !done || !aligned4(rows) || !aligned4(keep) || !aligned4(done)) return NSA_ERR_INVALID_ARG;
     return cuda_status(
         nsa::launch_pages_free(s, n, rows, keep, table, lens, ref, done, static_cast<cudaStream_t>(stream)));
 }
@@ -147,7 +151,7 @@ nsa_status nsa_pages_compact(const nsa_paged_config* cfg, void* k_pages, void* v
     if (st != NSA_OK) return st;
     if (!k_pages || !v_pages || !table || !lens || !ref || !remap || !n_live) return NSA_ERR_INVALID_ARG;
     if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned16(table) || !aligned16(lens) || !aligned16(ref) ||
-        !aligned16(remap) || !aligned16(workspace))
+        !aligned16(remap) || !aligned4(n_live) || !aligned16(workspace))
         return NSA_ERR_INVALID_ARG;
     if (!workspace || ws_bytes < nsa::pages_compact_ws_bytes(s)) return NSA_ERR_WORKSPACE;
     return cuda_status(nsa::launch_pages_compact(

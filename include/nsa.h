@@ -396,6 +396,8 @@ nsa_status nsa_window_attn_bwd(const nsa_window_config* cfg, const void* q, cons
  * break the rules above; the kernels do not follow them out of bounds (such an
  * id reads as rows of zeros and is not written, lengths are clamped), but what
  * they compute is then unspecified.
+ * Lists of rows and their results (src, dst, rows, keep, done) and the single
+ * results (short_pages, n_live) need 4-byte alignment only.
  * Calls on one cache are ordered by the caller (one stream).
  */
 typedef struct {

@@ -172,3 +172,21 @@ def test_waits_for_tensor_memory_name_the_registers():
         text = src.read_text()
         assert "tmem_wait_ld()" not in text, src.name
         assert "tmem_ld32(" not in text or "tmem_wait_ld32(" in text, src.name
+
+
+def test_fork_and_free_refuse_misaligned_books_and_lists(abi):
+    """The cache's books are 16-byte aligned as in every other call on it; lists, and the single results
+    of append and compaction, hold whole int32."""
+    cfg = _paged(abi)
+    for f, lists in [(abi.nsa_pages_fork, (0, 1, 5)), (abi.nsa_pages_free, (0, 1, 5))]:
+        for i in range(6):
+            args = [P] * 6
+            args[i] = P + (2 if i in lists else 4)
+            assert _status(abi, lambda: f(cfg, 1, *args)) == "NSA_ERR_INVALID_ARG", (f.__name__, i)
+        args = [P] * 6
+        args[3] = P + 4
+        assert _status(abi, lambda: f(cfg, 0, *args)) == "NSA_ERR_INVALID_ARG"
+    n = abi.nsa_paged_append_workspace_size(cfg)
+    assert _status(abi, lambda: abi.nsa_paged_append(cfg, *[P] * 8, P + 2, P, n)) == "NSA_ERR_INVALID_ARG"
+    n = abi.nsa_pages_compact_workspace_size(cfg)
+    assert _status(abi, lambda: abi.nsa_pages_compact(cfg, *[P] * 6, P + 2, P, n)) == "NSA_ERR_INVALID_ARG"
