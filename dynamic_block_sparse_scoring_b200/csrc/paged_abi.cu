@@ -69,8 +69,7 @@ nsa_status nsa_paged_attn_fwd(const nsa_paged_config* cfg, const void* q, const 
         !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
         return NSA_ERR_INVALID_ARG;
     // units (16 query rows of a sequence and KV head) are counted in 32 bits
-    if ((int64_t)s.Tq * s.G > INT32_MAX / 2 ||
-        (int64_t)s.B * s.Hkv * (((int64_t)s.Tq * s.G + 15) / 16) > INT32_MAX)
+    if ((int64_t)s.Tq * s.G > INT32_MAX / 2 || !nsa::fits32(s.B, s.Hkv, ((int64_t)s.Tq * s.G + 15) / 16))
         return NSA_ERR_UNSUPPORTED;
     if (!workspace || ws_bytes < nsa::paged_attn_ws_bytes(s)) return NSA_ERR_WORKSPACE;
     return cuda_status(nsa::launch_paged_attn(

@@ -24,7 +24,7 @@ nsa_status make_win_shape(const nsa_window_config* cfg, WinShape* s) {
     if (!(c.scale >= 1e-30f && c.scale <= 1e30f)) return NSA_ERR_INVALID_ARG;       // (NaN too)
     if (!nsa::supported_dqk(c.d_qk) || !nsa::supported_dv(c.d_v)) return NSA_ERR_UNSUPPORTED;
     // rows and planes are counted in 32 bits, and positions a tile behind the last one exist
-    if ((int64_t)c.batch * c.seqlen_q * c.h_q > INT32_MAX || (int64_t)c.batch * c.h_kv * c.seqlen_kv > INT32_MAX ||
+    if (!nsa::fits32(c.batch, c.seqlen_q, c.h_q) || !nsa::fits32(c.batch, c.h_kv, c.seqlen_kv) ||
         c.seqlen_kv > INT32_MAX - 1024)
         return NSA_ERR_UNSUPPORTED;
     s->B = c.batch;

@@ -190,3 +190,15 @@ def test_fork_and_free_refuse_misaligned_books_and_lists(abi):
     assert _status(abi, lambda: abi.nsa_paged_append(cfg, *[P] * 8, P + 2, P, n)) == "NSA_ERR_INVALID_ARG"
     n = abi.nsa_pages_compact_workspace_size(cfg)
     assert _status(abi, lambda: abi.nsa_pages_compact(cfg, *[P] * 6, P + 2, P, n)) == "NSA_ERR_INVALID_ARG"
+
+
+def test_sizes_whose_products_pass_64_bits_are_refused(abi):
+    """2^22 sequences of 2^21 tokens and heads: the product is 2^64, which must not count as 0."""
+    big = dict(batch=1 << 22, seqlen_q=1 << 21, seqlen_kv=1 << 21, h_q=1 << 21, h_kv=1 << 21, q_pos0=0)
+    for kw in [big, dict(big, seqlen_q=0), dict(big, batch=1 << 30, h_q=1 << 30, h_kv=1 << 30, seqlen_kv=16, seqlen_q=16)]:
+        cfg = _win(abi, **kw)
+        assert _status(abi, lambda: abi.nsa_window_bwd_workspace_size(cfg)) == "NSA_ERR_UNSUPPORTED"
+        assert _status(abi, lambda: abi.nsa_window_attn_fwd(cfg, P, P, P, P, P)) == "NSA_ERR_UNSUPPORTED"
+    cfg = _paged(abi, batch=1 << 30, max_pages=1, h_q=1 << 28, h_kv=1 << 14, seqlen_q=1 << 10)
+    assert (1 << 30) * (1 << 14) * (1 << 20) == 1 << 64          # sequences, KV heads, tiles of 16 rows
+    assert _status(abi, lambda: abi.nsa_paged_attn_fwd(cfg, *[P] * 7, P, 1 << 40)) == "NSA_ERR_UNSUPPORTED"
