@@ -283,3 +283,29 @@ def test_a_query_that_is_not_a_number_shows_in_every_output(dims):
         assert x[0, 50, 1].isnan().all() and x[0, 50, 0].isfinite().all() and x[0, 49, 1].isfinite().all()
     for x in (dk, dvv):
         assert x[0, 0, 43:51].isnan().any(-1).all() and x[0, 1].isfinite().all()
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128)], ids=str)
+@pytest.mark.parametrize("first", [0, 60, 190, 336])
+def test_dq_shows_the_part_of_every_single_key(first, dims):
+    """Keys first + c, c < 64, are unit vectors e_c and all others zero, so column c of dq is scale ds of
+    one key: a key too many or too few in any row changes its column by many times its bound."""
+    dqk, dv = dims
+    T, Hq, Hkv, W, ns = 400, 6, 2, 130, 70
+    g = torch.Generator(device="cuda")
+    g.manual_seed(15)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, v, d_out = r(1, T, Hq, dqk), r(1, Hkv, T, dv), r(1, T, Hq, dv)
+    k = torch.zeros(1, Hkv, T, dqk, dtype=torch.bfloat16, device="cuda")
+    c = torch.arange(64, device="cuda")
+    k[:, :, first + c, c] = 1
+    cfg = abi.window_config(1, T, T, Hq, Hkv, dqk, dv, W, ns)
+    out, lse = abi.window_forward(cfg, q, k, v)
+    dq = abi.window_backward(cfg, q, k, v, out, lse, d_out)[0]
+    vis = visible(T, T, 0, W, ns, "cuda")
+    value, bound = window_ref(q, k, v, vis, cfg.scale, d_out)["dq"]
+    check(dq, (value, bound), "dq")
+    part = vis[:, first:first + 64]                              # [T, 64]
+    ratio = (value.abs() / bound)[0, :, :, :64].transpose(1, 2)[part]
+    assert float(ratio.median()) > 10
+    assert not dq[0, :, :, :64].transpose(1, 2)[~part].any()
