@@ -323,9 +323,17 @@ def forward(cfg: NsaConfig, q, k, v, gates=None, idx=None, stream=None, pooled=N
 # Window attention with sink tokens, and the paged cache
 # ---------------------------------------------------------------------------
 
+def _counts(counts: int):
+    """counts: the bitwise or of a configuration's counts.  ctypes would take a count of 2^31 or more
+    modulo 2^32 (negative ones are refused by the entry points)."""
+    if counts >> 31 > 0:
+        raise ValueError("a count of the configuration does not fit 31 bits")
+
+
 def window_config(batch, seqlen_q, seqlen_kv, h_q, h_kv, d_qk, d_v, window, sink=0, q_pos0=0,
                   scale=None) -> NsaWindowConfig:
     """nsa_window_config (scale: 1/sqrt(d_qk) unless given)."""
+    _counts(batch | seqlen_q | seqlen_kv | q_pos0 | h_q | h_kv | d_qk | d_v | window | sink)
     return NsaWindowConfig(batch, seqlen_q, seqlen_kv, q_pos0, h_q, h_kv, d_qk, d_v, window, sink,
                            max(d_qk, 1) ** -0.5 if scale is None else scale, 0)
 
@@ -333,6 +341,7 @@ def window_config(batch, seqlen_q, seqlen_kv, h_q, h_kv, d_qk, d_v, window, sink
 def paged_config(batch, seqlen_q, h_q, h_kv, d_qk, d_v, page_size, n_pages, max_pages, window=0,
                  sink=0, scale=None) -> NsaPagedConfig:
     """nsa_paged_config (scale: 1/sqrt(d_qk) unless given)."""
+    _counts(batch | seqlen_q | h_q | h_kv | d_qk | d_v | page_size | n_pages | max_pages | window | sink)
     return NsaPagedConfig(batch, seqlen_q, h_q, h_kv, d_qk, d_v, page_size, n_pages, max_pages,
                           window, sink, max(d_qk, 1) ** -0.5 if scale is None else scale, 0)
 

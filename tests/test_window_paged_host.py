@@ -202,3 +202,15 @@ def test_sizes_whose_products_pass_64_bits_are_refused(abi):
     cfg = _paged(abi, batch=1 << 30, max_pages=1, h_q=1 << 28, h_kv=1 << 14, seqlen_q=1 << 10)
     assert (1 << 30) * (1 << 14) * (1 << 20) == 1 << 64          # sequences, KV heads, tiles of 16 rows
     assert _status(abi, lambda: abi.nsa_paged_attn_fwd(cfg, *[P] * 7, P, 1 << 40)) == "NSA_ERR_UNSUPPORTED"
+
+
+@pytest.mark.parametrize("big", [1 << 31, (1 << 32) + 5, 1 << 40])
+def test_configs_refuse_counts_that_do_not_fit(abi, big):
+    """A window or a number of sinks "over everything" must not be taken modulo 2^32."""
+    for kw in [dict(window=big), dict(sink=big), dict(seqlen_kv=big), dict(batch=big)]:
+        with pytest.raises(ValueError, match="31 bits"):
+            _win(abi, **kw)
+    for kw in [dict(window=big), dict(sink=big), dict(n_pages=big), dict(page_size=big)]:
+        with pytest.raises(ValueError, match="31 bits"):
+            _paged(abi, **kw)
+    assert _win(abi, window=2 ** 31 - 1).window == 2 ** 31 - 1
