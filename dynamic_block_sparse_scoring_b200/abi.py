@@ -330,20 +330,25 @@ def _counts(counts: int):
         raise ValueError("a count of the configuration does not fit 31 bits")
 
 
+_I32_MAX = 2 ** 31 - 1          # a window or a number of sinks beyond it covers every key, as this does
+
+
 def window_config(batch, seqlen_q, seqlen_kv, h_q, h_kv, d_qk, d_v, window, sink=0, q_pos0=0,
                   scale=None) -> NsaWindowConfig:
     """nsa_window_config (scale: 1/sqrt(d_qk) unless given)."""
-    _counts(batch | seqlen_q | seqlen_kv | q_pos0 | h_q | h_kv | d_qk | d_v | window | sink)
-    return NsaWindowConfig(batch, seqlen_q, seqlen_kv, q_pos0, h_q, h_kv, d_qk, d_v, window, sink,
+    _counts(batch | seqlen_q | seqlen_kv | q_pos0 | h_q | h_kv | d_qk | d_v)
+    return NsaWindowConfig(batch, seqlen_q, seqlen_kv, q_pos0, h_q, h_kv, d_qk, d_v,
+                           min(window, _I32_MAX), min(sink, _I32_MAX),
                            max(d_qk, 1) ** -0.5 if scale is None else scale, 0)
 
 
 def paged_config(batch, seqlen_q, h_q, h_kv, d_qk, d_v, page_size, n_pages, max_pages, window=0,
                  sink=0, scale=None) -> NsaPagedConfig:
     """nsa_paged_config (scale: 1/sqrt(d_qk) unless given)."""
-    _counts(batch | seqlen_q | h_q | h_kv | d_qk | d_v | page_size | n_pages | max_pages | window | sink)
+    _counts(batch | seqlen_q | h_q | h_kv | d_qk | d_v | page_size | n_pages | max_pages)
     return NsaPagedConfig(batch, seqlen_q, h_q, h_kv, d_qk, d_v, page_size, n_pages, max_pages,
-                          window, sink, max(d_qk, 1) ** -0.5 if scale is None else scale, 0)
+                          min(window, _I32_MAX), min(sink, _I32_MAX),
+                          max(d_qk, 1) ** -0.5 if scale is None else scale, 0)
 
 
 def nsa_window_attn_fwd(cfg, q, k, v, out, lse=None, stream=None):

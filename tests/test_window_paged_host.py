@@ -206,11 +206,13 @@ def test_sizes_whose_products_pass_64_bits_are_refused(abi):
 
 @pytest.mark.parametrize("big", [1 << 31, (1 << 32) + 5, 1 << 40])
 def test_configs_refuse_counts_that_do_not_fit(abi, big):
-    """A window or a number of sinks "over everything" must not be taken modulo 2^32."""
-    for kw in [dict(window=big), dict(sink=big), dict(seqlen_kv=big), dict(batch=big)]:
+    """No count is taken modulo 2^32; a window or a number of sinks that large covers every key."""
+    for kw in [dict(seqlen_kv=big), dict(batch=big)]:
         with pytest.raises(ValueError, match="31 bits"):
             _win(abi, **kw)
-    for kw in [dict(window=big), dict(sink=big), dict(n_pages=big), dict(page_size=big)]:
+    for kw in [dict(n_pages=big), dict(page_size=big)]:
         with pytest.raises(ValueError, match="31 bits"):
             _paged(abi, **kw)
-    assert _win(abi, window=2 ** 31 - 1).window == 2 ** 31 - 1
+    for make in (_win, _paged):
+        cfg = make(abi, window=big, sink=big)
+        assert cfg.window == cfg.sink == 2 ** 31 - 1
