@@ -23,6 +23,9 @@
 // a small problem) is cut into items over its queries, whose fp32 partial
 // sums window_bwd_join_kernel adds in order.
 //
+// A query tile whose first row sees few keys (FEW_KEYS) is walked twice in DQ: the first walk sums ds,
+// which corrects delta, the second builds dQ with that.
+//
 // Warps (384 threads): 0 TMA, 1 MMA issue (one lane), 2-3 the rows' (lse,
 // delta), 4-7 and 8-11 two warpgroups taking the steps in turn, one thread per
 // resident row.  The issue order S(i+1) D(i+1) | gradients(i) gives the softmax
@@ -75,7 +78,9 @@ struct Smem {
     // the products, 32 bytes a row: a constant [BM] of the residents, then per stage [BN] for S, [BN] for D
     static constexpr int AUX_OFF = T_OFF + NST * T_BYTES;
     static constexpr int EXT_A = BM * 32, EXT_B = BN * 32;
-    static constexpr int AUX_BYTES = MODE == DQ ? 2 * BM * 8 : EXT_A + NST * 2 * EXT_B;
+    // DQ: behind them, per (work, warpgroup) of two works each row's sum of ds of the first walk
+    static constexpr int SUM_OFF = AUX_OFF + 2 * BM * 8;
+    static constexpr int AUX_BYTES = MODE == DQ ? 2 * BM * 8 + 4 * BM * 4 : EXT_A + NST * 2 * EXT_B;
     static constexpr int BAR_OFF = AUX_OFF + AUX_BYTES;
     static_assert(AUX_OFF % 1024 == 0, "swizzled rows");
     static constexpr int ALLOC = BAR_OFF + 512 + 1024;
@@ -86,7 +91,7 @@ struct Smem {
 
 struct Bars {
     uint64_t r_full, r_empty, t_full[4], t_empty[4], s_full[2], d_full[2], d_read[2], p_full[2];
-    uint64_t acc_full, acc_free, aux_full[2], aux_empty[2], drain;
+    uint64_t acc_full, acc_free, aux_full[2], aux_empty[2], sum_full, drain;
     uint32_t tmem;
     int abort;
     int large;          // DKV: a row with |lse| > LARGE_LSE has been among the steps so far
@@ -132,11 +137,18 @@ __host__ __device__ __forceinline__ void tile_queries(const WinShape& s, int u0,
 // One work item: the steps of a query tile (DQ) or of a share of a key tile's queries (DKV).
 struct Work {
     int b, kvh, n;      // n: steps
+    int m;              // DQ: steps of a walk over the keys, n or, where the tile is walked twice, n / 2
     int first;          // DQ: first token of the query tile.  DKV: first key of the tile
     int base, rot;      // DKV: first token, and which step's place the first step takes
     int nst, sl, lo;    // DQ: sink steps, sinks before the window, first key of the window's steps
     int slot;           // DKV: partial-sum slot, -1: the only item of its key tile
 
+    // DQ: first key of step i; does the step hold sinks before the window?
+    __device__ __forceinline__ int key(int i) const {
+        const int j = i < m ? i : i - m;
+        return j < nst ? j * BN : lo + (j - nst) * BN;
+    }
+    __device__ __forceinline__ bool sink_step(int i) const { return (i < m ? i : i - m) < nst; }
     // DKV: first token of step i.  Turned (rot >= 0), the steps run backwards from rot on and
     // around, so that CTAs whose key tiles share queries come to them at the same time: block
     // b of tok tokens is taken at step (last block - b) mod n.
@@ -159,7 +171,8 @@ __device__ __forceinline__ bool decode_work(const Args& a, int w, Work* k) {
         k->sl = min(s.ns, k->lo);
         k->nst = ceil_div(k->sl, BN);
         if (k->lo < k->nst * BN) k->lo = k->sl = k->nst = 0;        // they meet: one range from 0
-        k->n = k->nst + (pl - k->lo) / BN + 1;
+        k->m = k->nst + (pl - k->lo) / BN + 1;
+        k->n = visible_keys(s, pf) <= FEW_KEYS ? 2 * k->m : k->m;
         return true;
     }
     const int n_s = planes * a.p.nsk * a.p.sp_s;
@@ -303,6 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc::mbar_init(&bar.acc_full, 1);
         tc::mbar_init(&bar.acc_free, 8);
+        tc::mbar_init(&bar.sum_full, 8);
         tc::mbar_init(&bar.drain, 1);
         bar.abort = 0;
         bar.large = 0;
@@ -376,8 +390,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const CUtensorMap* m = c < L::QC ? &map_t1 : &map_t2;
                         const int x = 64 * (c < L::QC ? c : c - L::QC);
                         if (MODE == DQ)
-                            tc::tma_load_3d(dst + c * TCHUNK, m, &bar.t_full[st], x,
-                                            i < k.nst ? i * BN : k.lo + (i - k.nst) * BN, plane);
+                            tc::tma_load_3d(dst + c * TCHUNK, m, &bar.t_full[st], x, k.key(i), plane);
                         else
                             tc::tma_load_4d(dst + c * TCHUNK, m, &bar.t_full[st], x, h0, k.token(i, a.tok), k.b);
                     }
@@ -483,7 +496,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         __syncwarp();
                     }
                     const uint64_t gd = tc::desc_at(g_desc, gst * L::T_BYTES);
-                    const uint32_t tA = tmem + b * 64, tAq = MODE == DKV ? tA + 32 : tA, acc = i > 0 ? 1u : 0u;
+                    const uint32_t tA = tmem + b * 64, tAq = MODE == DKV ? tA + 32 : tA;
+                    const uint32_t acc = i > 0 && (MODE == DKV || i != k.m) ? 1u : 0u;      // (the second walk starts anew)
                     if (i == 0 && !warp_wait(&bar.acc_free, (works & 1) ^ 1)) { ok = false; break; }
                     if (!p_soon && !warp_wait(&bar.p_full[b], (e >> 1) & 1)) { ok = false; break; }
                     tc::fence_after_sync();
@@ -623,7 +637,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int tt = r / s.G;
         TileRows tile_rows;
         if (MODE == DQ) tile_rows.init(r, s.G);
-        uint32_t g = 0, works = 0, n = 0;
+        uint32_t g = 0, works = 0, n = 0, walks = 0;
         bool ok = true;
         if (MODE == DKV) pdl_wait();
         for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
@@ -649,8 +663,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             bool clamp = MODE == DQ && __any_sync(0xffffffffu, fabsf(mine.x) > LARGE_LSE);
             uint64_t sc2 = clamp ? tc::f2_pack(1.f, 1.f) : tc::f2_pack(a.scale_log2, a.scale_log2);
             const float neg = clamp ? 0.f : -mine.x;
-            const uint64_t lse2 = tc::f2_pack(neg, neg), del2 = tc::f2_pack(-mine.y, -mine.y);
+            const uint64_t lse2 = tc::f2_pack(neg, neg);
+            uint64_t del2 = tc::f2_pack(-mine.y, -mine.y), ds_sum[2] = {0, 0};
             for (int i = 0; i < k.n; ++i, ++g) {
+                if (MODE == DQ && i == k.m) {       // the first walk is done
+                    float* sum = reinterpret_cast<float*>(sm + L::SUM_OFF) + (walks & 1) * 2 * BM;
+                    float s0, s1;
+                    tc::f2_unpack(tc::f2_add(ds_sum[0], ds_sum[1]), s0, s1);
+                    sum[wg * BM + r] = s0 + s1;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.sum_full);
+                    if (!warp_wait(&bar.sum_full, walks & 1)) { ok = false; break; }
+                    ++walks;
+                    const float delta = mine.y + (sum[r] + sum[BM + r]);
+                    del2 = tc::f2_pack(-delta, -delta);
+                    if (wg == 0 && tt < min(a.tok, s.Tq - k.first))        // for DKV, over the one of the rounded out
+                        a.delta[((long long)k.b * s.Tq + k.first + tt) * s.Hq + k.kvh * s.G + (r - tt * s.G)] = delta;
+                }
                 if ((int)(g & 1) != wg) continue;
                 if (MODE == DKV) {
                     // (not reused before this step's P is read: makes the flag of its rows visible)
@@ -666,8 +695,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // visible columns [lo, hi] and [0, sk)
                 int lo, hi, sk = 0;
                 if (MODE == DQ) {
-                    const int u0 = i < k.nst ? i * BN : k.lo + (i - k.nst) * BN;
-                    if (i < k.nst) {
+                    const int u0 = k.key(i);
+                    if (k.sink_step(i)) {
                         lo = 0;
                         hi = k.sl - 1 - u0;
                     } else {
@@ -718,13 +747,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bar.d_read[wg]);
                 }
-                // bf16 weights and ds: half a step, 2^-9 relative of each term
+                // bf16 weights and ds: half a step, 2^-8 relative of each term at most
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
                     const uint64_t p2 = tc::f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
                     const uint64_t d2 = tc::f2_pack(__uint_as_float(y[c]), __uint_as_float(y[c + 1]));
                     float e0, e1;
-                    tc::f2_unpack(tc::f2_mul(p2, MODE == DQ ? tc::f2_add(d2, del2) : d2), e0, e1);
+                    const uint64_t ds2 = tc::f2_mul(p2, MODE == DQ ? tc::f2_add(d2, del2) : d2);
+                    if (MODE == DQ) ds_sum[(c >> 1) & 1] = tc::f2_add(ds_sum[(c >> 1) & 1], ds2);
+                    tc::f2_unpack(ds2, e0, e1);
                     y[c / 2] = tc::pack_bf16x2(e0, e1);
                     x[c / 2] = tc::pack_bf16x2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]));
                 }

@@ -133,7 +133,21 @@ __global__ void __launch_bounds__(128) window_dq_kernel(WinShape s, const __nv_b
     load_row(out + (size_t)w * s.dv, nv, lane, acc);
     load_row(d_out + (size_t)w * s.dv, nv, lane, df);
     load_row(q + (size_t)w * s.dqk, nq, lane, qf);
-    const float dl = warp_sum(dot(acc, df)), ls = bwd_lse(lse[w]);
+    float dl = warp_sum(dot(acc, df));
+    const float ls = bwd_lse(lse[w]);
+    if (visible_keys(s, r.t) <= FEW_KEYS) {
+        float ds = 0.f;
+        for_keys(s, r.t, [&](int u0, int n) {
+            for (int j = 0; j < n; ++j) {
+                float2 kf[MAXP], vf[MAXP];
+                load_row(k + (r.plane * s.Tk + u0 + j) * s.dqk, nq, lane, kf);
+                load_row(v + (r.plane * s.Tk + u0 + j) * s.dv, nv, lane, vf);
+                const float p = expf(at_most_0(warp_sum(dot(qf, kf)) * s.scale - ls));
+                ds = fmaf(p, warp_sum(dot(df, vf)) - dl, ds);
+            }
+        });
+        dl += ds;
+    }
     if (lane == 0) delta[w] = dl;
 #pragma unroll
     for (int i = 0; i < MAXP; ++i) acc[i] = make_float2(0.f, 0.f);

@@ -363,7 +363,10 @@ nsa_status nsa_window_attn_fwd(const nsa_window_config* cfg, const void* q, cons
  *   dq [B, Tq, Hq, d_qk] = scale sum_u ds_u k_u
  *   dk [B, Hkv, Tkv, d_qk] = scale sum_{t, h} ds_u q      dv_u = sum_{t, h} p_u d_out
  * all bf16 and overwritten (rows of dk / dv that no query sees get 0), summed
- * in fp32 over the group's heads and every query and rounded once at the end.
+ * in fp32 over the group's heads and every query and rounded once at the end;
+ * on the tensor cores p and ds enter their products rounded to bf16.  delta
+ * reads the rounded out; rows that see at most 64 keys, where that would show
+ * in ds, correct it by the sum of their ds in fp32.
  * p is rebuilt from lse, whose 24 bits move it by a relative |lse| 2^-20 at
  * most (half a bf16 step at |lse| = 2^12); p stays in [0, 1] whatever the
  * scores, and a key that has a row's whole weight keeps it.
@@ -426,7 +429,7 @@ typedef struct {
  * A query without keys (an empty sequence, a position below 0) gets out = 0
  * and lse = -inf.  The work is cut over the keys of all sequences by the
  * lengths found on the device, so one captured graph serves a growing cache;
- * the shares of one query are joined by their log-sum-exps in fp32, in a fixed
+ * the shares of one query are joined by their maxima and sums in fp32, in a fixed
  * order.  Weights enter the value product rounded to bf16.  Needs
  * nsa_paged_workspace_size() bytes of workspace, which need not start at zero.
  */
