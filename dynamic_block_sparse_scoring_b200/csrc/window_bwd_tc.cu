@@ -61,6 +61,7 @@ constexpr int RCHUNK = 16384, TCHUNK = 8192;    // 128 / 64 rows x 64 columns of
 constexpr int THREADS = 384;
 constexpr uint64_t WAIT_NS = 1000000000ull;
 constexpr int SMS = 148;                        // the split of key tiles is planned for this many SMs
+constexpr int MAX_FLAGS = 256;                  // most CTAs of the dq kernel
 // Least steps of an item of a split key tile: 1000 tokens, 4 heads on 1, d 64, window 128 + 4
 // took 35.3 us at 8, 32.5 at 4, 32.4 at 2; fewer steps only mean more partial sums.
 constexpr int MIN_CHUNK = 4;
@@ -94,7 +95,7 @@ struct Bars {
     uint64_t acc_full, acc_free, aux_full[2], aux_empty[2], sum_full, drain;
     uint32_t tmem;
     int abort;
-    int large;          // DKV: a row with |lse| > LARGE_LSE has been among the steps so far
+    int large;          // DQ: a row with |lse| > LARGE_LSE has been among the CTA's
 };
 
 // How the key tiles are cut into items (DKV): key tiles below nsk hold sinks
@@ -117,6 +118,8 @@ struct Args {
     __nv_bfloat16* dk;
     __nv_bfloat16* dv;
     float* part;        // partial sums [slot][BM][DV + DQK]
+    int* flags;         // [n_flags] Bars::large of the dq kernel's CTAs
+    int n_flags;
     int tok;            // tokens per query tile (DQ) or per step (DKV)
     int n_tt;           // query tiles per (sequence, KV head) (DQ)
     int n_work;
@@ -293,9 +296,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     volatile int* large = &bar.large;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WinShape& s = a.s;
-    // What follows in the stream may start on the SMs that this grid leaves idle: of its
-    // results the DKV kernel reads delta alone, and waits for it.  There every role waits for this
-    // grid's end before its first wait that needs delta, so that the bounded waits count the
+    // What follows in the stream may start on the SMs that this grid leaves idle: of its results
+    // the DKV kernel reads delta and the flags, and waits for them.  There every role waits for this
+    // grid's end before its first wait that needs them, so that the bounded waits count the
     // time of their own grid only; the copies of the first stages go before.
     pdl_launch();
 
@@ -611,7 +614,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int r = lane + 32 * e, half = (r >> 2) & 1;
                     uint4* x = reinterpret_cast<uint4*>(sm + L::AUX_OFF + L::EXT_A + st * 2 * L::EXT_B + r * 32);
-                    if (fabsf(v[e].x) > LARGE_LSE && v[e].x != 3e38f) *large = 1;
                     // (of a row without a query: -3e38, not times 1 / scale, which could pass fp32)
                     x[half] = three(v[e].x == 3e38f ? -3e38f : -v[e].x * inv_scale);
                     x[half ^ 1] = make_uint4(0, 0, 0, 0);
@@ -639,7 +641,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (MODE == DQ) tile_rows.init(r, s.G);
         uint32_t g = 0, works = 0, n = 0, walks = 0;
         bool ok = true;
-        if (MODE == DKV) pdl_wait();
+        bool clamp = false;                         // a large lse could lift exponents above 0 (bwd_lse)
+        if (MODE == DKV) {
+            pdl_wait();
+            for (int i = lane; i < a.n_flags; i += 32) clamp |= a.flags[i] != 0;
+            clamp = __any_sync(0xffffffffu, clamp);
+        }
         for (int round = 0, w; ok && (w = dealt(round)) < a.n_work; ++round) {
             Work k;
             if (!decode_work<MODE>(a, w, &k)) continue;
@@ -658,10 +665,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) tc::mbar_arrive(&bar.aux_empty[buf]);
                 ++n;
             }
-            // exponents are scores times sc2 + lse2, or, where a large lse could lift them above 0, taken
-            // and clamped beforehand
-            bool clamp = MODE == DQ && __any_sync(0xffffffffu, fabsf(mine.x) > LARGE_LSE);
-            uint64_t sc2 = clamp ? tc::f2_pack(1.f, 1.f) : tc::f2_pack(a.scale_log2, a.scale_log2);
+            if (MODE == DQ) {                       // (infinity: not a row)
+                clamp = __any_sync(0xffffffffu, fabsf(mine.x) > LARGE_LSE && mine.x != INFINITY);
+                if (clamp) *large = 1;
+            }
+            // exponents are scores times sc2 + lse2, or, to be clamped, taken beforehand
+            const uint64_t sc2 = clamp ? tc::f2_pack(1.f, 1.f) : tc::f2_pack(a.scale_log2, a.scale_log2);
             const float neg = clamp ? 0.f : -mine.x;
             const uint64_t lse2 = tc::f2_pack(neg, neg);
             uint64_t del2 = tc::f2_pack(-mine.y, -mine.y), ds_sum[2] = {0, 0};
@@ -681,12 +690,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                         a.delta[((long long)k.b * s.Tq + k.first + tt) * s.Hq + k.kvh * s.G + (r - tt * s.G)] = delta;
                 }
                 if ((int)(g & 1) != wg) continue;
-                if (MODE == DKV) {
-                    // (not reused before this step's P is read: makes the flag of its rows visible)
-                    if (!warp_wait(&bar.t_full[g % L::NST], (g / L::NST) & 1)) { ok = false; break; }
-                    clamp = *large != 0;
-                    sc2 = clamp ? tc::f2_pack(1.f, 1.f) : tc::f2_pack(a.scale_log2, a.scale_log2);
-                }
                 if (!warp_wait(&bar.s_full[wg], (g >> 1) & 1)) { ok = false; break; }
                 tc::fence_after_sync();
                 uint32_t x[64], y[64];
@@ -839,6 +842,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     if (warp == 1) tc::tmem_dealloc(tmem, 512);
+    if (MODE == DQ && threadIdx.x == 0) a.flags[blockIdx.x] = *large;
 }
 
 // Adds the items' partial sums of a split key tile, in order: one thread per
@@ -927,7 +931,8 @@ cudaError_t launch_impl(Args a, const __nv_bfloat16* q, const __nv_bfloat16* k, 
         a.tok = tok_q;
         a.n_tt = ceil_div(s.Tq, tok_q);
         a.n_work = a.n_tt * planes;
-        kernel<<<std::min(a.n_work, nsm), THREADS, L::ALLOC, st>>>(q128, do128, k64, v64, a);
+        a.n_flags = std::min(std::min(a.n_work, nsm), MAX_FLAGS);
+        kernel<<<a.n_flags, THREADS, L::ALLOC, st>>>(q128, do128, k64, v64, a);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -948,7 +953,7 @@ cudaError_t launch_impl(Args a, const __nv_bfloat16* q, const __nv_bfloat16* k, 
 
 size_t window_bwd_tc_part_bytes(const WinShape& s) {
     const Split p = make_split(s);
-    return up256(part_slots(s, p) * BM * (s.dqk + s.dv) * 4);
+    return MAX_FLAGS * 4 + up256(part_slots(s, p) * BM * (s.dqk + s.dv) * 4);
 }
 
 cudaError_t launch_window_bwd_tc(const WinShape& s, const __nv_bfloat16* q, const __nv_bfloat16* k,
@@ -965,8 +970,9 @@ cudaError_t launch_window_bwd_tc(const WinShape& s, const __nv_bfloat16* q, cons
     a.dq = dq;
     a.dk = dk;
     a.dv = dv;
-    a.part = part;
-    a.tok = a.n_tt = a.n_work = 0;
+    a.flags = reinterpret_cast<int*>(part);
+    a.part = part + MAX_FLAGS;
+    a.tok = a.n_tt = a.n_work = a.n_flags = 0;
     // Neighbouring key tiles read the same rows of q and d_out.  While these fit the L2 (126 MB)
     // beside everything else, each tile takes them in its own order (4096 tokens, 16 heads, d 128,
     // 34 MB: 358 us a training step, 368 turned: every CTA asks for the same lines at once); larger

@@ -111,6 +111,39 @@ def test_backward_weights_stay_below_one(dims, scale):
     check(got[2], (ref, (2 * H + 2.0 ** -16) * size + 1e-6), "dv")
 
 
+
+@pytest.mark.parametrize("dims", [(6, 2, 128, 128), (160, 160, 64, 64), (4, 2, 256, 256)], ids=str)
+@pytest.mark.parametrize("large", [(5,), (0, 3, 130, 299)])
+def test_a_few_rows_with_large_scores_among_ordinary_ones(large, dims):
+    """Queries `large` are 2^20 times a unit vector whose scores are whole numbers (one key has all the
+    weight), the others have none of that column; dv holds both, dq of the ordinary rows and the other
+    columns of dk are as without the large rows."""
+    Hq, Hkv, dqk, dv = dims
+    T, W, ns = 300, 90, 7
+    g = torch.Generator(device="cuda")
+    g.manual_seed(25)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    q, k, v, d_out = r(1, T, Hq, dqk), r(1, Hkv, T, dqk), r(1, Hkv, T, dv), r(1, T, Hq, dv)
+    q[..., 0] = 0
+    q[:, large] = 0
+    q[:, large, :, 0] = 2.0 ** 20
+    for h in range(Hkv):
+        k[0, h, :, 0] = (torch.randperm(T, generator=g, device="cuda") - T // 2).to(torch.bfloat16)
+    cfg = abi.window_config(1, T, T, Hq, Hkv, dqk, dv, W, ns)
+    out, lse = abi.window_forward(cfg, q, k, v)
+    dq, dk, dvv = abi.window_backward(cfg, q, k, v, out, lse, d_out)
+    vis = visible(T, T, 0, W, ns, "cuda")
+    some = torch.zeros_like(d_out)
+    some[:, large] = d_out[:, large]
+    ref = window_ref(q, k, v, vis, cfg.scale, d_out - some)
+    part = window_ref(q, k, v, vis, cfg.scale, some)["dv"][0]
+    size = window_ref(q, k, v, vis, cfg.scale, some.abs())["dv"][0]
+    check(dvv, (ref["dv"][0] + part, ref["dv"][1] + (2 * H + 2.0 ** -16) * size), "dv")
+    rest = [t for t in range(T) if t not in large]
+    check(dq[:, rest], (ref["dq"][0][:, rest], ref["dq"][1][:, rest]), "dq")
+    check(dk[..., 1:], (ref["dk"][0][..., 1:], ref["dk"][1][..., 1:]), "dk")
+
+
 @pytest.mark.parametrize("scale", [1e6, 1e9, 1e30])
 @pytest.mark.parametrize("new, page, lens", [(1, 16, [700, 3, 64]), (3, 64, [2100])])
 def test_paged_attention_gives_the_weight_to_the_largest_scores(scale, new, page, lens):
