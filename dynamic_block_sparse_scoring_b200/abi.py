@@ -469,7 +469,8 @@ _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def window_forward(cfg: NsaWindowConfig, q, k, v):
-    """Window attention with sink tokens on the current stream: (out bf16, lse fp32)."""
+    """Window attention with sink tokens on the current stream: (out bf16, lse fp32).  Not recorded by
+    autograd, whatever the inputs require: window_backward gives the gradients."""
     B, Tq, Hq, Hkv, Tk, d, dv = (cfg.batch, cfg.seqlen_q, cfg.h_q, cfg.h_kv, cfg.seqlen_kv, cfg.d_qk, cfg.d_v)
     dev = _device(("q", q, (B, Tq, Hq, d), _BF16), ("k", k, (B, Hkv, Tk, d), _BF16),
                   ("v", v, (B, Hkv, Tk, dv), _BF16))
@@ -523,7 +524,8 @@ def paged_attention(cfg: NsaPagedConfig, q, k_pages, v_pages, table, lens):
 
 def paged_append(cfg: NsaPagedConfig, k_new, v_new, k_pages, v_pages, table, lens, ref, n_new=None):
     """Appends up to cfg.seqlen_q tokens per sequence, in place, on the current stream.  Returns
-    short_pages [1] int32 on the device: 0, or what was missing (then nothing has changed)."""
+    short_pages [1] int32 on the device: 0, the pages that were missing, or -1 where a row would outgrow
+    the table (then nothing has changed)."""
     new = (cfg.batch, cfg.h_kv, cfg.seqlen_q)
     extra = () if n_new is None else (("n_new", n_new, (cfg.batch,), _I32),)
     dev = _device(("k_new", k_new, new + (cfg.d_qk,), _BF16), ("v_new", v_new, new + (cfg.d_v,), _BF16),

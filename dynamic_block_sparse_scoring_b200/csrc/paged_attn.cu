@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(Dim<DQK, DV>::WARPS * 32, 1) paged_attn_kernel
 #pragma unroll
                 for (int j = 0; j < 4; ++j) p[j] = tc::ex2(x[j] - ref);
                 l[e] = l[e] * alpha[e] + ((p[0] + p[1]) + (p[2] + p[3]));
-                pf[e] = tc::pack_bf16x2(p[0], p[1]);        // bf16 weights: half a step, 2^-9 relative,
-                pf[2 + e] = tc::pack_bf16x2(p[2], p[3]);    // independent per key
+                pf[e] = tc::pack_bf16x2(p[0], p[1]);        // bf16 weights: half a step, 2^-8 relative
+                pf[2 + e] = tc::pack_bf16x2(p[2], p[3]);    // at most, independent per key
             }
             if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll

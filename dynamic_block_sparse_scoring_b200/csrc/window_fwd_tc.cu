@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                            v_desc = tc::sdesc_sw128(tc::smem_u32(sm + L::V_OFF), CHUNK, 1024);
             auto uwait = [&](uint64_t* b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)); };
             // The loops stay rolled: the short code is a little faster than the unrolled one (at the
-            // two sizes of the head comment 175.6 us against 177.0 and 425 against 434).
+            // two sizes of the head comment 175.6 us against 177.0 and 424.9 against 433.9).
             uint32_t ks = 0, kph = 0, vs = 0, vph = 0;      // stage and phase of the next key / value tile
             uint32_t nq = 0, np = 0;                        // bit t: parity of tile t's next Q, next P
             bool ok = true;
@@ -533,7 +533,7 @@ cudaError_t launch_impl(const WinShape& s, const __nv_bfloat16* q, const __nv_bf
 }  // namespace
 
 // What fits TMEM (512 columns) and shared memory, and a token's heads in half a query tile.
-// Everything else runs on FFMA, 100 times slower where both serve (16384 tokens, 64 heads
+// Everything else runs on FFMA, 160 times slower where both serve (16384 tokens, 64 heads
 // on 4, 192/128, window 512 + 64: 68.4 ms against 0.42).
 bool window_tc_supported(const WinShape& s) {
     return s.dqk <= 192 && s.dv <= 128 && s.G <= 64;

@@ -368,8 +368,8 @@ nsa_status nsa_window_attn_fwd(const nsa_window_config* cfg, const void* q, cons
  * reads the rounded out; rows that see at most 64 keys, where that would show
  * in ds, correct it by the sum of their ds in fp32.
  * p is rebuilt from lse, whose 24 bits move it by a relative |lse| 2^-20 at
- * most (half a bf16 step at |lse| = 2^12); p stays in [0, 1] whatever the
- * scores, and a key that has a row's whole weight keeps it.
+ * most (half a bf16 step at |lse| = 2^12); whatever the scores, p passes 1 by
+ * no more than 2^-6, and a key that has a row's whole weight keeps it.
  * No atomics: the same inputs give the same bits.  Needs
  * nsa_window_bwd_workspace_size() bytes of workspace (delta, and the partial
  * sums of keys that many queries see); nothing in it needs to start at zero.
@@ -430,7 +430,9 @@ typedef struct {
  * and lse = -inf.  The work is cut over the keys of all sequences by the
  * lengths found on the device, so one captured graph serves a growing cache;
  * the shares of one query are joined by their maxima and sums in fp32, in a fixed
- * order.  Weights enter the value product rounded to bf16.  Needs
+ * order.  Weights enter the value product rounded to bf16.  Every key and value
+ * of a sequence must be finite, and |scale q.k| below 1e38: a key that another
+ * query of the call sees enters the value product with weight 0.  Needs
  * nsa_paged_workspace_size() bytes of workspace, which need not start at zero.
  */
 nsa_status nsa_paged_workspace_size(const nsa_paged_config* cfg, size_t* bytes);
