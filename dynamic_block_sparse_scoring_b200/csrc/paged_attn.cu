@@ -21,7 +21,7 @@
 // need a few percent of the tensor cores at full HBM rate, and a warp keeps
 // its whole state in registers, without a CTA-wide hand-over per tile.
 // Bound by HBM: 64 sequences of up to 32768 keys, 64 heads on 4, 192/128:
-// 400 us, 6.5 TB/s in a burst; 48 x 4 tokens, 32 heads on 8, d 128, window
+// 394-431 us, 6.1-6.6 TB/s; 48 x 4 tokens, 32 heads on 8, d 128, window
 // 4096 + 16, pages of 16: 136 us, 5.6 TB/s, the join 6 of them.  One sequence of
 // 1000 keys is two launches of dependent loads: 10.8 us (7.8 without the join).
 #include <math.h>

@@ -36,8 +36,9 @@
 // of MMA, for the 6 KB that they read, and the copies write 40 KB a step.
 // Measured in bursts, forward included: 8192 tokens, 64 heads on 4, 192/128,
 // window 512 + 64: 980 us, 684 TFLOP/s; 4096 tokens, 16 heads, d 128, fully
-// causal: 342 us, 703 TFLOP/s (counting five products of the backward, not the
-// seven done); 1114 and 371 us back to back under the power cap.
+// causal: 363 us, 662 TFLOP/s (counting five products of the backward, not the
+// seven done); 1119-1148 and 371-380 us back to back under the power cap.  Of these
+// the clamp of large scores and the sums of ds are 0.5 % each.
 #include <math.h>
 
 #include <algorithm>

@@ -28,9 +28,10 @@
 // MACs per key tile at 4096 a clock, its exponentials 2 x 16384 at 16 a clock;
 // in fact by the round trip softmax -> P V, Q K^T -> softmax of each tile, in
 // which both pipes are about half busy (without any softmax 136 us of 175).
-// Measured in bursts: 2 x 8192 tokens, 16 heads, d 128, window 1000 + 16:
-// 175 us, 730 TFLOP/s; 16384 tokens, 64 heads on 4, 192/128, window 512 + 64:
-// 420 us, 905 TFLOP/s (196 and 486 us back to back under the power cap).
+// Measured in bursts, on two cards: 2 x 8192 tokens, 16 heads, d 128, window
+// 1000 + 16: 177 and 186 us, 722 and 687 TFLOP/s; 16384 tokens, 64 heads on 4,
+// 192/128, window 512 + 64: 417 and 430 us, 911 and 884 TFLOP/s (196-202 and
+// 485-496 us back to back under the power cap).
 #include <math.h>
 
 #include <algorithm>
